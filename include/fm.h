@@ -450,6 +450,172 @@ fm_status fm_decode_attention(const float* q, const uint8_t* mem, int64_t row_st
 fm_status fm_toy_decoder_update(const float* hidden, const float* attn_out, int B, int H, float eps,
                                 float* hidden_out, cudaStream_t stream);
 
+/* --------------------------------------------------- 4-bit paged cache
+ * The keys and values that a decoding model attends to, held in 4 bits in
+ * pages of a pool: what a token costs is 136 bytes for a key and value head
+ * of 128, where bf16 takes 512.  The pages of the retriever's README keep
+ * the cache itself out of view ("compressed KV chunks" and their records are
+ * all they describe), so the layout is this library's own:
+ *
+ *   record   128 e2m1 codes (two to a byte, the even dimension in the low
+ *            half) and four e8m0 scales, one for each 32 dimensions:
+ *            value = e2m1(code) * 2^(scale - 127).  The stored scale byte is
+ *            the least that keeps the group's largest magnitude within 6
+ *            times the scale, at least 1 and at most 252; a group of zeros
+ *            has 0, a group with a NaN or an infinity has 255 and reads as
+ *            NaN.  Codes are the nearest values, ties to the even code; a
+ *            zero has no sign.
+ *   block    the records of page_size tokens of one kv head: page_size * 64
+ *            code bytes (token after token), then page_size * 4 scale bytes.
+ *   page     one block for each kv head, head h at + h * head_stride_bytes;
+ *            page p at + p * page_stride_bytes of the pool.  Keys and values
+ *            have a pool each, with the same strides.
+ *   table    page_table [B, max_pages] int32: position j of row b lies in
+ *            page page_table[b, j / page_size], slot j % page_size.  An
+ *            entry outside [0, n_pages) is a page that is not there. */
+typedef struct fm_kv4_cache {
+  uint8_t* k_pages;           /* device, 16-byte aligned */
+  uint8_t* v_pages;           /* device, 16-byte aligned */
+  int64_t page_stride_bytes;  /* a multiple of 16, >= page_size * 68 */
+  int64_t head_stride_bytes;  /* a multiple of 16, >= page_size * 68 */
+  int n_pages;                /* pages in each pool */
+  int page_size;              /* tokens in a page: a multiple of 16, at most 1024 */
+  int n_kv_heads;             /* 1..1024 */
+  int B;                      /* rows of the page table, 1..65535 */
+  int max_pages;              /* entries of a row; max_pages * page_size <= 2^30 */
+  int64_t page_table_stride;  /* elements between rows of the table, >= max_pages */
+  const int32_t* page_table;  /* device */
+} fm_kv4_cache;
+/* Blocks do not overlap: page_stride >= n_kv_heads * head_stride (page after
+ * page), or head_stride >= n_pages * page_stride (a pool for each head);
+ * anything else is FM_ERR_INVALID_ARG. */
+
+enum { FM_F32 = 0, FM_BF16 = 1, FM_F16 = 2 };
+
+/* The rotary frequencies of query prep (README "Architecture": RoPE with
+ * YaRN), for the calls below: f_j in fp64, j < rope_dim / 2, into host memory
+ * (cfg's rope_* fields are read, the others are ignored; rope_dim even, up to
+ * 128).  A host-side call. */
+fm_status fm_rope_frequencies(const fm_config* cfg, double* inv_freq_host);
+
+/* Appends T tokens: the keys rotated by their positions on the way, keys and
+ * values quantised into the records of their slots; optionally the queries
+ * rotated into q_out, and the values that the new records stand for.
+ *
+ * Token t goes to row seq[t], position pos[t].  A token with seq[t] outside
+ * [0, B), pos[t] outside [0, max_pages * page_size) or a page that is not
+ * there is padding: nothing is written for it, in the cache or in the
+ * outputs.  Two tokens of one call must not name the same slot (the slot then
+ * holds a mixture of the two).
+ *
+ * Rotation: half-split pairs of the last rope_dim dimensions, as query prep
+ * does it: x1' = x1 c - x2 s, x2' = x2 c + x1 s with c, s = fp32(cos, sin of
+ * the fp64 angle positions[t] * inv_freq[j]).  The products and their sum are
+ * exact to 2^-46 before the one rounding to the code (or to q_out's type). */
+typedef struct fm_kv4_append_desc {
+  int dtype;                  /* FM_F32, FM_BF16, FM_F16: of k, v, q and q_out */
+  int T;                      /* tokens, >= 1 */
+  int n_q_heads;              /* heads of q, 1..1024; ignored when q is NULL */
+  const void* k;              /* [T, n_kv_heads, 128] device; the heads of a token are packed */
+  const void* v;
+  const void* q;              /* [T, n_q_heads, 128] device or NULL */
+  int64_t k_stride, v_stride, q_stride, q_out_stride; /* elements between tokens (times the element size: a multiple
+                                                          of 16); pointers 16-byte aligned */
+  const int32_t* seq;         /* [T] device */
+  const int64_t* pos;         /* [T] device */
+  const int64_t* positions;   /* [T] device: positions to rotate by, or NULL (= pos) */
+  const double* inv_freq;     /* [rope_dim / 2] device */
+  int rope_dim;               /* 0 (no rotation), 64 or 128 */
+  void* q_out;                /* [T, n_q_heads, 128] device; may be q (with the same stride) */
+  void* k_hat;                /* [T, n_kv_heads, 128] bf16 device or NULL: the stored keys' values (exact) */
+  void* v_hat;                /* the same for the values */
+} fm_kv4_append_desc;
+
+fm_status fm_kv4_append(const fm_kv4_cache* cache, const fm_kv4_append_desc* d, cudaStream_t stream);
+
+/* Attention of Tq new tokens of every row over its cached keys and values
+ * (their own included: append them first):
+ *
+ *   query t of row b stands at position p = kv_len[b] - Tq + t and sees the
+ *   positions j with kv_start[b] <= j <= p, and p - j < window if window > 0,
+ *   whose page is there; with idx, only those listed for its row
+ *   x = scale * q . k_j;  x = softcap * tanh(x / softcap) if softcap > 0;
+ *   x = x + slopes[h] * (j - p) if slopes;  out = sum softmax(x)_j v_j
+ *
+ * A query that sees nothing gives 0 (kv_len 0, a position below 0, an empty
+ * window or list).  What a query does not see is not touched by it, whatever
+ * its records hold.  Query head h uses kv head h / (n_q_heads / n_kv_heads).
+ * Dot products, statistics and sums are fp32; fp32 queries and the softmax
+ * weights enter the products at 2^-22 or better, 16-bit ones exactly, their
+ * weights at 2^-11. */
+typedef struct fm_kv4_attn_desc {
+  int dtype;                  /* FM_F32, FM_BF16, FM_F16: of q and out */
+  int Tq;                     /* query tokens of every row, 1..64 */
+  int n_q_heads;              /* a multiple of n_kv_heads, at most 1024 */
+  const void* q;              /* [B, Tq, n_q_heads, 128] device, 16-byte aligned, heads packed */
+  int64_t q_stride;           /* elements between tokens (b, t) -> (b, t + 1) -> ...: a multiple of 16 bytes */
+  void* out;                  /* [B, Tq, n_q_heads, 128] device, 16-byte aligned, packed (written) */
+  const int32_t* kv_len;      /* [B] device: cached tokens of a row, clamped to [0, max_len] */
+  const int32_t* kv_start;    /* [B] device or NULL: the first visible position (a document's start, left padding) */
+  int max_len;                /* a bound of kv_len, 1..max_pages * page_size: sizes the launch */
+  const int32_t* idx;         /* [B, max_sel] device or NULL: visible positions (fm_compact_mask's list); one that is
+                                 listed twice counts twice, one outside [0, kv_len) not at all */
+  const int32_t* count;       /* [B] device, with idx: entries of a row, clamped to [0, max_sel] */
+  int max_sel;
+  float scale;                /* finite */
+  float softcap;              /* 0: none; > 0 */
+  const float* slopes;        /* [n_q_heads] device or NULL */
+  int window;                 /* 0: none; > 0 */
+} fm_kv4_attn_desc;
+
+/* Bytes of device workspace fm_kv4_attention needs (it depends on B, Tq, the
+ * heads, max_len and max_sel only); 0 for a descriptor that it would refuse. */
+size_t fm_kv4_attention_workspace_bytes(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d);
+
+/* ws: caller-owned, 16-byte aligned; contents on entry irrelevant.  Calls that
+ * may overlap need a workspace each. */
+fm_status fm_kv4_attention(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/* Appends indexer keys: the compressed_k records that fm_score reads (README
+ * "compressed_k format"), from the keys that a compressor produced.
+ *   x = k[t, l] (rotated as in fm_kv4_append if rope_dim > 0), then, with
+ *   hadamard, the normalised 128-point Walsh-Hadamard transform (the query's
+ *   last step; a rotation of both sides leaves their products as they are);
+ *   scale = max|x| / 448 in fp32, codes = e4m3(x * (1 / scale)), nearest even
+ * into record chunk[t] of row row[t] of comp_k[l].  A key whose scale would be
+ * below 2^-126 is stored as zeros with scale 0; one with a NaN or an infinity
+ * gets a NaN scale.  A token with row[t] outside [0, B) or chunk[t] outside
+ * [0, N) is padding: nothing is written.  Two tokens of one call must not
+ * name the same record.
+ * k [T, L, 128] device, 16-byte aligned, token_stride elements between tokens
+ * (times the element size: a multiple of 16); 1 <= L <= 4; comp_k: array of L
+ * device pointers (host array), 4-byte aligned, row b at + b *
+ * row_stride_bytes (a multiple of 4, >= N * 132); positions [T] int64 and
+ * inv_freq [rope_dim / 2] fp64 device with rope_dim 64 or 128. */
+fm_status fm_index_append(const void* k, int dtype, int64_t token_stride, int T, int L, const int32_t* row,
+                          const int32_t* chunk, const int64_t* positions, const double* inv_freq, int rope_dim,
+                          int hadamard, uint8_t* const* comp_k, int64_t row_stride_bytes, int B, int N,
+                          cudaStream_t stream);
+
+/* Residual addition, RMSNorm and an 8-bit output with scales: what a decoder
+ * layer does between its blocks, for projections that read e4m3
+ * (fm_toy_decoder_update with a gain, the model's types and a narrow output).
+ *   z = x + residual (fp32; residual NULL: x);  sum_out = z in the type
+ *   y = z * (mean(z^2) + eps)^-1/2 * gain (gain NULL: 1)
+ *   scale[t, g] = max|y| over group g / 448;  codes = e4m3(y * (1 / scale))
+ * A group whose scale would be below 2^-126 is stored as zeros with scale 0; a
+ * row whose sum of squares is not finite in fp32 (a NaN, an infinity, values
+ * past 2^63) has NaN scales.
+ * x, residual [T, H] device, 16-byte aligned, x_stride / residual_stride elements between rows (times
+ * the element size: a multiple of 16); gain [H] of the same type; sum_out
+ * [T, H] packed or NULL, may be x or residual when that is packed; codes
+ * [T, H] packed; scales [T, H / group] fp32.  H a multiple of 128, at most
+ * 65536; group 128 or H. */
+fm_status fm_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                             const void* gain, int dtype, int T, int H, float eps, int group, void* sum_out,
+                             uint8_t* codes, float* scales, cudaStream_t stream);
+
 /* Synchronises `stream` and returns FM_ERR_DEVICE if a kernel launched on this
  * context recorded an error since the last call (the record is cleared), or
  * if one of the context-free kernels of the current device did (decode

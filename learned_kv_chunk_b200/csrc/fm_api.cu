@@ -132,6 +132,22 @@ void fm_config_default(fm_config* c) {
   c->cta_pairs = 0;
 }
 
+fm_status fm_rope_frequencies(const fm_config* cfg, double* inv_freq_host) {
+  if (!cfg || !inv_freq_host || cfg->rope_dim < 2 || cfg->rope_dim > kHeadDim || cfg->rope_dim % 2)
+    return FM_ERR_INVALID_ARG;
+  if (!(cfg->rope_base > 1.0) || !(cfg->rope_factor >= 1.0) || !(cfg->rope_orig_max_pos > 0) ||
+      !(cfg->rope_beta_fast > 0) || !(cfg->rope_beta_slow > 0))
+    return FM_ERR_INVALID_ARG;
+  try {
+    std::vector<double> f;
+    yarn_frequencies(*cfg, f);
+    std::memcpy(inv_freq_host, f.data(), f.size() * sizeof(double));
+  } catch (...) {  // no exception leaves a C entry
+    return FM_ERR_OOM;
+  }
+  return FM_OK;
+}
+
 fm_status fm_create(const fm_config* cfg, const fm_layer_weights* w, int device, fm_ctx** out) {
   if (!out) return FM_ERR_INVALID_ARG;
   *out = nullptr;

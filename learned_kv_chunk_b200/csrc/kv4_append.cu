@@ -1,0 +1,395 @@
+// kv4_append.cu -- the producers of what the library's other calls read: keys
+// and values appended to the 4-bit paged cache with the position rotation on
+// the way (fm_kv4_append), and indexer keys as the 132-byte records that the
+// scoring pass reads (fm_index_append).
+//
+// Mathematics.  A head of 128 dimensions belongs to 16 lanes, 8 consecutive
+// dimensions each.  Rotation pairs (D - rd + j, D - rd/2 + j) lie rd/16 lanes
+// apart, so one shuffle brings a lane its partners.
+//   * A rotated value is x1 c - x2 s with c, s in fp32 and x of 8, 11 or 24
+//     bits: each product is split into its fp32 rounding and the exact rest
+//     (one fma), the two are added as a pair, and the pair is rounded once to
+//     fp32 "to odd": truncated, the last bit set if anything was cut off.  A
+//     number rounded to odd compares with any border of fewer bits as the
+//     exact one does and rounds to any shorter type as the exact one does, so
+//     codes, scales and narrow queries are those of the exact rotation.  Plain
+//     fp32 would move one value in about ten million across a code's border,
+//     by a whole step of the 4-bit type.
+//   * Scale: the least power of two 2^e with max|x| <= 6 * 2^e (6 is the
+//     largest e2m1 value), read from the exponent and mantissa bits of the
+//     group's maximum; x * 2^-e is exact.
+#include <cmath>
+
+#include "kv4.cuh"
+
+namespace fm {
+namespace {
+
+constexpr int kAppThreads = 256;              // 16 heads of 16 lanes each
+constexpr int kAppUnits = kAppThreads / 16;
+
+// fp64 angle positions * f; cos and sin rounded to fp32 once, as query prep does.
+__device__ __forceinline__ float2 rope_cos_sin(int64_t position, double f) {
+  double s, c;
+  sincos((double)position * f, &s, &c);
+  return make_float2((float)c, (float)s);
+}
+
+// a * c - b * s (NEG) or a * c + b * s as the rounded sum `hi`, and the sum
+// rounded to odd.
+template <bool NEG>
+__device__ __forceinline__ void rot_pair(float a, float c, float b, float s, float& hi, float& odd) {
+  const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
+  const float bs = NEG ? -b : b;
+  const float q = __fmul_rn(bs, s), qe = __fmaf_rn(bs, s, -q);
+  // p + q as a pair, then the products' rests
+  const float t = __fadd_rn(p, q);
+  const float z = __fsub_rn(t, p);
+  const float te = __fadd_rn(__fsub_rn(p, __fsub_rn(t, z)), __fsub_rn(q, z));
+  const float lo0 = __fadd_rn(te, __fadd_rn(pe, qe));
+  hi = __fadd_rn(t, lo0);
+  const float lo = __fsub_rn(lo0, __fsub_rn(hi, t));
+  odd = hi;
+  if (lo != 0.f && isfinite(hi)) {
+    uint32_t u = __float_as_uint(hi);
+    if ((lo < 0.f) != (hi < 0.f)) u -= 1;  // the exact value is nearer to zero: truncate
+    odd = __uint_as_float(u | 1u);
+  }
+}
+
+// Rotates the lane's 8 values of a head (lane l of 16 has dims 8l .. 8l+7).
+// cs: cos, sin of the token for j < RD / 2.
+template <int RD>
+__device__ __forceinline__ void rotate8(float (&x)[8], float (&odd)[8], int l, const float2* cs) {
+  if constexpr (RD == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd[i] = x[i];
+  } else {
+    constexpr int kHalfLanes = RD / 16;              // lanes of half a pair range
+    constexpr int kFirst = (kKvDim - RD) / 8;        // first rotated lane
+    const bool in = l >= kFirst;
+    const bool second = in && l >= kFirst + kHalfLanes;
+    const int j0 = in ? 8 * (second ? l - kFirst - kHalfLanes : l - kFirst) : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, x[i], kHalfLanes);
+      const float2 w = cs[j0 + i];
+      float hi, o;
+      if (second) rot_pair<false>(x[i], w.x, other, w.y, hi, o);
+      else rot_pair<true>(x[i], w.x, other, w.y, hi, o);
+      odd[i] = in ? o : x[i];
+      x[i] = in ? hi : x[i];
+    }
+  }
+}
+
+// Quantises the lane's 8 values: the group's scale byte (4 lanes share one)
+// and 8 codes.
+__device__ __forceinline__ void quant8(const float (&x)[8], uint32_t& byte, uint32_t& codes) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(x[i]));
+  m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  if (!(m < INFINITY)) {
+    byte = 255u;
+    codes = 0u;
+    return;
+  }
+  // m = f * 2^(E - 127), 1 <= f < 2: 6 * 2^e = 1.5 * 2^(e + 2) >= m
+  const uint32_t u = __float_as_uint(m);
+  int e = (int)(u >> 23) - 127 - 2 + ((u & 0x7fffffu) > 0x400000u ? 1 : 0);
+  e = max(-126, min(125, e));
+  byte = m > 0.f ? (uint32_t)(e + 127) : 0u;
+  const float r = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e: e in [-126, 125], a normal number
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i] * r, x[2 * i + 1] * r), __NV_E2M1, cudaRoundNearest)
+         << (8 * i);
+  // a zero keeps no sign
+  const uint32_t nz = (w | (w >> 1) | (w >> 2)) & 0x11111111u;
+  codes = w & (0x77777777u | (nz << 3));
+}
+
+// The value of e2m1 code c (4 bits), fp32.
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+  const float v = e ? __uint_as_float(((e + 126u) << 23) | (m << 22)) : 0.5f * (float)m;
+  return (c & 8u) ? -v : v;
+}
+
+struct AppendArgs {
+  Kv4View c;
+  const void* x[3];          // q, k, v
+  int64_t stride[3];
+  const int32_t* seq;
+  const int64_t* pos;
+  const int64_t* positions;
+  const double* inv_freq;
+  int n_q;
+  void* q_out;
+  int64_t q_out_stride;
+  __nv_bfloat16* hat[2];     // k, v
+};
+
+// One CTA a token: its cosines and sines once, then 16 heads at a time, each
+// by 16 lanes.
+template <class T, int RD>
+__global__ void __launch_bounds__(kAppThreads) kv4_append_kernel(const AppendArgs a) {
+  __shared__ float2 cs[RD ? RD / 2 : 1];
+  const int t = blockIdx.x;
+  const int row = __ldg(a.seq + t);
+  const int64_t pos = __ldg(a.pos + t);
+  if (row < 0 || row >= a.c.B || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return;
+  const int pg = (int)pos / a.c.page_size, slot = (int)pos - pg * a.c.page_size;
+  const int page = __ldg(a.c.table + row * a.c.table_stride + pg);
+  if (page < 0 || page >= a.c.n_pages) return;
+  if (RD && threadIdx.x < RD / 2)
+    cs[threadIdx.x] = rope_cos_sin(a.positions ? __ldg(a.positions + t) : pos, __ldg(a.inv_freq + threadIdx.x));
+  __syncthreads();
+  const int l = threadIdx.x & 15;
+  const int n_kv = a.c.n_heads, units = a.n_q + 2 * n_kv;
+  // a warp's two units run together (the shuffles need both halves): round up
+  for (int u0 = 0; u0 < units; u0 += kAppUnits) {
+    const int u = u0 + (threadIdx.x >> 4);
+    const bool on = u < units;
+    const int which = u < a.n_q ? 0 : u < a.n_q + n_kv ? 1 : 2;
+    const int h = which == 0 ? u : which == 1 ? u - a.n_q : u - a.n_q - n_kv;
+    float x[8] = {}, odd[8];
+    if (on) load8(static_cast<const T*>(a.x[which]) + t * a.stride[which] + h * kKvDim + 8 * l, x);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
+    rotate8<RD>(y, odd, l, cs);
+    if (which == 2) {  // values are stored as they are
+#pragma unroll
+      for (int i = 0; i < 8; ++i) odd[i] = x[i];
+    }
+    uint32_t byte, codes;
+    quant8(odd, byte, codes);
+    uint32_t b = byte << (8 * (l >> 2));  // the record's four scales, from lanes 0, 4, 8, 12
+    b |= __shfl_xor_sync(0xffffffffu, b, 4);
+    b |= __shfl_xor_sync(0xffffffffu, b, 8);
+    if (!on) continue;
+    if (which == 0) {
+      // fp32: the rounded sum; narrower types round once, from the odd one
+      T* o = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * kKvDim + 8 * l;
+      if (sizeof(T) == 4) store8(o, y);
+      else store8(o, odd);
+    } else {
+      uint8_t* blk = (which == 1 ? a.c.k : a.c.v) + page * a.c.page_stride + h * a.c.head_stride;
+      *reinterpret_cast<uint32_t*>(blk + slot * kKvCodeBytes + 4 * l) = codes;
+      if (l == 0)
+        *reinterpret_cast<uint32_t*>(blk + a.c.page_size * kKvCodeBytes + slot * kKvScaleBytes) = b;
+      if (__nv_bfloat16* hat = a.hat[which - 1]) {
+        const float s = e8m0_value(byte);
+        float val[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) val[i] = e2m1_value((codes >> (4 * i)) & 15u) * s;
+        store8(hat + ((int64_t)t * n_kv + h) * kKvDim + 8 * l, val);
+      }
+    }
+  }
+}
+
+struct IndexArgs {
+  const void* k;
+  int64_t stride;
+  const int32_t* row;
+  const int32_t* chunk;
+  const int64_t* positions;
+  const double* inv_freq;
+  uint8_t* comp_k[kMaxLayers];
+  int64_t row_stride;
+  int T, L, B, N, hadamard;
+};
+
+constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
+
+// The e4m3 codes of a lane's values over the scale of their amax.
+__device__ __forceinline__ float e4m3_scale(float amax, float& inv) {
+  float scale = amax / 448.f;
+  inv = scale >= kMinNormal ? 1.f / scale : 0.f;
+  if (scale < kMinNormal) scale = 0.f;
+  if (!(scale < INFINITY)) scale = nan_f32();
+  return scale;
+}
+
+// 16 lanes a key, 16 keys a CTA.
+template <class T, int RD>
+__global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexArgs a) {
+  __shared__ float2 cs[kAppUnits][RD ? RD / 2 : 1];
+  const int64_t u = (int64_t)blockIdx.x * kAppUnits + (threadIdx.x >> 4);
+  const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const bool in = u < (int64_t)a.T * a.L;
+  const int t = in ? (int)(u / a.L) : 0, layer = in ? (int)(u - (int64_t)t * a.L) : 0;
+  const int row = in ? __ldg(a.row + t) : -1, chunk = in ? __ldg(a.chunk + t) : -1;
+  const bool on = row >= 0 && row < a.B && chunk >= 0 && chunk < a.N;
+  float x[8] = {}, odd[8];
+  if (on) {
+    load8(static_cast<const T*>(a.k) + t * a.stride + layer * kKvDim + 8 * l, x);
+    if (RD) {
+      const int64_t p = __ldg(a.positions + t);
+      for (int j = l; j < RD / 2; j += 16) cs[w][j] = rope_cos_sin(p, __ldg(a.inv_freq + j));
+    }
+  }
+  __syncwarp();
+  rotate8<RD>(x, odd, l, cs[w]);
+  if (a.hadamard) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!(i & s)) {
+          const float p = x[i], q = x[i + s];
+          x[i] = p + q;
+          x[i + s] = p - q;
+        }
+#pragma unroll
+    for (int s = 1; s < 16; s <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float o = __shfl_xor_sync(0xffffffffu, x[i], s);
+        x[i] = (l & s) ? o - x[i] : x[i] + o;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= 0.08838834764831845f;  // 128^-1/2
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(x[i]));
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
+  if (!on) return;
+  float inv;
+  const float scale = e4m3_scale(m, inv);
+  uint32_t c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    c[i] = lo | (hi << 16);
+  }
+  uint32_t* rec = reinterpret_cast<uint32_t*>(a.comp_k[layer] + row * a.row_stride + (int64_t)chunk * kRecord);
+  rec[2 * l] = c[0];
+  rec[2 * l + 1] = c[1];
+  if (l == 0) rec[32] = __float_as_uint(scale);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <class F>
+fm_status by_rope_dim(int rd, F&& f) {
+  if (rd == 0) return f(std::integral_constant<int, 0>{});
+  if (rd == 64) return f(std::integral_constant<int, 64>{});
+  return f(std::integral_constant<int, 128>{});
+}
+
+}  // namespace
+
+fm_status check_kv4_cache(const fm_kv4_cache* c) {
+  if (!c || !c->k_pages || !c->v_pages || !c->page_table) return FM_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->B < 1 || c->B > 65535 || c->max_pages < 1)
+    return FM_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16) return FM_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_pages * c->page_size > ((int64_t)1 << 30)) return FM_ERR_INVALID_ARG;
+  if (c->page_table_stride < c->max_pages) return FM_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || c->page_stride_bytes % 16 || c->head_stride_bytes % 16 ||
+      (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
+    return FM_ERR_ALIGNMENT;
+  const int64_t block = (int64_t)c->page_size * kKvBytes;
+  const int64_t most = (int64_t)1 << 45;  // keeps every product below in range
+  if (c->page_stride_bytes < block || c->head_stride_bytes < block || c->page_stride_bytes > most ||
+      c->head_stride_bytes > most)
+    return FM_ERR_INVALID_ARG;
+  if (c->page_stride_bytes < c->n_kv_heads * c->head_stride_bytes &&
+      c->head_stride_bytes / c->page_stride_bytes < c->n_pages)
+    return FM_ERR_INVALID_ARG;
+  return FM_OK;
+}
+
+}  // namespace fm
+
+using namespace fm;
+
+extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_desc* d, cudaStream_t stream) {
+  if (fm_status s = check_kv4_cache(c)) return s;
+  if (!d || !d->k || !d->v || !d->seq || !d->pos || d->T < 1 || !dtype_ok(d->dtype)) return FM_ERR_INVALID_ARG;
+  if (d->q && (!d->q_out || d->n_q_heads < 1 || d->n_q_heads > 1024)) return FM_ERR_INVALID_ARG;
+  if (d->rope_dim != 0 && d->rope_dim != 64 && d->rope_dim != 128) return FM_ERR_UNSUPPORTED;
+  if (d->rope_dim && !d->inv_freq) return FM_ERR_INVALID_ARG;
+  const int es = dtype_size(d->dtype);
+  const int64_t kv_width = (int64_t)c->n_kv_heads * kKvDim;
+  if (d->k_stride < kv_width || d->v_stride < kv_width) return FM_ERR_INVALID_ARG;
+  if (d->q && (d->q_stride < (int64_t)d->n_q_heads * kKvDim || d->q_out_stride < (int64_t)d->n_q_heads * kKvDim))
+    return FM_ERR_INVALID_ARG;
+  if (d->q == d->q_out && d->q && d->q_stride != d->q_out_stride) return FM_ERR_INVALID_ARG;
+  if (!aligned16(d->k) || !aligned16(d->v) || (d->k_stride * es) % 16 || (d->v_stride * es) % 16 ||
+      (d->q && (!aligned16(d->q) || !aligned16(d->q_out) || (d->q_stride * es) % 16 || (d->q_out_stride * es) % 16)) ||
+      !aligned16(d->k_hat) || !aligned16(d->v_hat) || (reinterpret_cast<uintptr_t>(d->seq) & 3u) ||
+      (reinterpret_cast<uintptr_t>(d->pos) & 7u) || (reinterpret_cast<uintptr_t>(d->positions) & 7u) ||
+      (reinterpret_cast<uintptr_t>(d->inv_freq) & 7u))
+    return FM_ERR_ALIGNMENT;
+  AppendArgs a = {};
+  a.c = kv4_view(*c);
+  a.x[0] = d->q; a.x[1] = d->k; a.x[2] = d->v;
+  a.stride[0] = d->q_stride; a.stride[1] = d->k_stride; a.stride[2] = d->v_stride;
+  a.seq = d->seq;
+  a.pos = d->pos;
+  a.positions = d->positions;
+  a.inv_freq = d->inv_freq;
+  a.n_q = d->q ? d->n_q_heads : 0;
+  a.q_out = d->q_out;
+  a.q_out_stride = d->q_out_stride;
+  a.hat[0] = static_cast<__nv_bfloat16*>(d->k_hat);
+  a.hat[1] = static_cast<__nv_bfloat16*>(d->v_hat);
+  return by_dtype(d->dtype, [&](auto* tag) {
+    using T = std::remove_pointer_t<decltype(tag)>;
+    return by_rope_dim(d->rope_dim, [&](auto rd) {
+      kv4_append_kernel<T, decltype(rd)::value><<<d->T, kAppThreads, 0, stream>>>(a);
+      note_launch();
+      return check_launch();
+    });
+  });
+}
+
+extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_stride, int T, int L, const int32_t* row,
+                                     const int32_t* chunk, const int64_t* positions, const double* inv_freq,
+                                     int rope_dim, int hadamard, uint8_t* const* comp_k, int64_t row_stride_bytes,
+                                     int B, int N, cudaStream_t stream) {
+  if (!k || !row || !chunk || !comp_k || T < 1 || L < 1 || L > kMaxLayers || B < 1 || N < 1 || !dtype_ok(dtype))
+    return FM_ERR_INVALID_ARG;
+  if (rope_dim != 0 && rope_dim != 64 && rope_dim != 128) return FM_ERR_UNSUPPORTED;
+  if (rope_dim && (!positions || !inv_freq)) return FM_ERR_INVALID_ARG;
+  if (token_stride < (int64_t)L * kKvDim || row_stride_bytes < (int64_t)N * kRecord) return FM_ERR_INVALID_ARG;
+  if ((int64_t)T * L > ((int64_t)1 << 34)) return FM_ERR_INVALID_ARG;
+  if (!aligned16(k) || (token_stride * dtype_size(dtype)) % 16 || row_stride_bytes % 4 ||
+      (reinterpret_cast<uintptr_t>(row) & 3u) || (reinterpret_cast<uintptr_t>(chunk) & 3u) ||
+      (reinterpret_cast<uintptr_t>(positions) & 7u) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+    return FM_ERR_ALIGNMENT;
+  IndexArgs a = {};
+  for (int l = 0; l < L; ++l) {
+    if (!comp_k[l]) return FM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(comp_k[l]) & 3u) return FM_ERR_ALIGNMENT;
+    a.comp_k[l] = comp_k[l];
+  }
+  a.k = k;
+  a.stride = token_stride;
+  a.row = row;
+  a.chunk = chunk;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.row_stride = row_stride_bytes;
+  a.T = T; a.L = L; a.B = B; a.N = N;
+  a.hadamard = hadamard != 0;
+  const unsigned grid = (unsigned)(((int64_t)T * L + kAppUnits - 1) / kAppUnits);
+  return by_dtype(dtype, [&](auto* tag) {
+    using E = std::remove_pointer_t<decltype(tag)>;
+    return by_rope_dim(rope_dim, [&](auto rd) {
+      index_append_kernel<E, decltype(rd)::value><<<grid, kAppThreads, 0, stream>>>(a);
+      note_launch();
+      return check_launch();
+    });
+  });
+}

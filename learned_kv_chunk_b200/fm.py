@@ -22,6 +22,8 @@ FM_ERR_CUDA, FM_ERR_OOM, FM_ERR_DEVICE = 4, 5, 6
 FM_ENSEMBLE_MAX, FM_ENSEMBLE_MEAN = 0, 1
 MODES = {"max": FM_ENSEMBLE_MAX, "mean": FM_ENSEMBLE_MEAN}
 FM_TOPK_SHARD_BINS = 2048
+FM_KV4_TOKEN_BYTES = 68  # a record of the 4-bit cache: 64 code bytes and 4 scale bytes
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 class fm_config(ctypes.Structure):
@@ -60,6 +62,30 @@ class fm_device_staging(ctypes.Structure):
                 ("n_valid", ctypes.c_void_p), ("q", ctypes.c_void_p), ("fused_w", ctypes.c_void_p),
                 ("ens", ctypes.c_void_p), ("keep_topk", ctypes.c_void_p), ("keep_thr", ctypes.c_void_p),
                 ("topk_ws", ctypes.c_void_p), ("topk_ws_bytes", ctypes.c_size_t)]
+
+
+class fm_kv4_cache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_stride_bytes", ctypes.c_int64),
+                ("head_stride_bytes", ctypes.c_int64), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("B", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_table_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p)]
+
+
+class fm_kv4_append_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("T", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("seq", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("rope_dim", ctypes.c_int), ("q_out", ctypes.c_void_p),
+                ("k_hat", ctypes.c_void_p), ("v_hat", ctypes.c_void_p)]
+
+
+class fm_kv4_attn_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("Tq", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("kv_start", ctypes.c_void_p), ("max_len", ctypes.c_int), ("idx", ctypes.c_void_p),
+                ("count", ctypes.c_void_p), ("max_sel", ctypes.c_int), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int)]
 
 
 class FMError(RuntimeError):
@@ -107,6 +133,12 @@ def _load():
         "fm_topk_shard_pick": (I, [I, I, I, P, P, S, P]),
         "fm_topk_shard_ties": (I, [P, I, I, P, P, S, P]),
         "fm_topk_shard_mask": (I, [P, I, I, P, I, P, P, S, P]),
+        "fm_rope_frequencies": (I, [ctypes.POINTER(fm_config), P]),
+        "fm_kv4_append": (I, [P, P, P]),
+        "fm_kv4_attention_workspace_bytes": (S, [P, P]),
+        "fm_kv4_attention": (I, [P, P, P, S, P]),
+        "fm_index_append": (I, [P, I, I64, I, I, P, P, P, P, I, I, P, I64, I, I, P]),
+        "fm_add_rmsnorm_fp8": (I, [P, I64, P, I64, P, I, I, I, F, I, P, P, P, P]),
         "fm_sync_status": (I, [P, P]),
         "fm_strerror": (ctypes.c_char_p, [I]),
         "fm_last_cuda_error": (I, []),
@@ -536,6 +568,313 @@ def fm_select_topk_sharded(ens_local: torch.Tensor, k: int, n_valid_local: Optio
         sh.pick(p)
     eq_all = ex.all_gather(sh.ties())
     return sh.mask(eq_all, ex.rank)
+
+
+# ------------------------------------------------- the 4-bit paged cache
+
+
+class _On:
+    """Where a call runs: the device its tensors are on, and the stream (the
+    device's current one unless the caller names another).  As a context it
+    makes that device the current one for the C call.  Memory that the call
+    allocates comes from the stream's own pool, and the tensors of a call on a
+    side stream are recorded there, so that none is handed out again while the
+    kernels still use it."""
+
+    __slots__ = ("index", "stream", "side", "back")
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        if dev.type != "cuda":
+            raise ValueError("the tensors must be CUDA tensors")
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"the tensors must be on one device, got {dev} and {t.device}")
+        self.index, self.side, self.back = dev.index, None, -1
+        if stream is None:
+            self.stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        else:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            self.stream = stream.cuda_stream
+            if self.stream != torch._C._cuda_getCurrentRawStream(dev.index):
+                self.side = stream
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+
+    def new(self, make, shape, dtype):
+        """make = torch.empty or torch.zeros."""
+        dev = torch.device("cuda", self.index)
+        if self.side is None:
+            return make(shape, dtype=dtype, device=dev)
+        with torch.cuda.stream(self.side):
+            t = make(shape, dtype=dtype, device=dev)
+        t.record_stream(torch.cuda.current_stream(dev))
+        return t
+
+    def __enter__(self):
+        self.back = torch._C._cuda_exchangeDevice(self.index)
+        return self
+
+    def __exit__(self, *exc):
+        torch._C._cuda_exchangeDevice(self.back)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _like(t: torch.Tensor, shape, dtype, name: str):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _heads(t: torch.Tensor, T: int, name: str, dtype=None) -> int:
+    """[T, heads, 128] with packed heads -> the stride between tokens, in elements."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != 128 or t.dtype not in DTYPES:
+        raise ValueError(f"{name} must be [{T}, heads, 128] fp32, bf16 or fp16, got {t.dtype} {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128):
+        raise ValueError(f"the heads of a token of {name} must be packed")
+    return t.stride(0) if T > 1 else t.shape[1] * 128
+
+
+def _kv4_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor) -> fm_kv4_cache:
+    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8 or k_pages.dim() != 3:
+        raise ValueError("the pages must be uint8 [n_pages, n_kv_heads, page_size * 68]")
+    n_pages, n_heads, block = k_pages.shape
+    if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    if block % FM_KV4_TOKEN_BYTES or k_pages.stride(2) != 1:
+        raise ValueError("a page's block must be page_size * 68 contiguous bytes")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be int32 [B, max_pages] with contiguous rows")
+    B, max_pages = page_table.shape
+    head = k_pages.stride(1) if n_heads > 1 else block
+    page = k_pages.stride(0) if n_pages > 1 else max(n_heads * head, block)
+    return fm_kv4_cache(k_pages.data_ptr(), v_pages.data_ptr(), page, head, n_pages, block // FM_KV4_TOKEN_BYTES,
+                        n_heads, B, max_pages, page_table.stride(0) if B > 1 else max_pages, page_table.data_ptr())
+
+
+def _check_freq(inv_freq: Optional[torch.Tensor]) -> int:
+    if inv_freq is None:
+        return 0
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector (fm_rope_frequencies)")
+    return 2 * inv_freq.numel()
+
+
+def fm_rope_frequencies(device=None, rope_dim: int = 64, **overrides) -> torch.Tensor:
+    """Query prep's rotary frequencies (YaRN; the shipped constants unless
+    overridden: rope_base, rope_factor, rope_orig_max_pos, rope_beta_fast,
+    rope_beta_slow) for the append calls: float64 [rope_dim / 2] on `device`
+    (the host without one)."""
+    cfg = fm_config_default()
+    cfg.rope_dim = int(rope_dim)
+    for k, v in overrides.items():
+        if not k.startswith("rope_") or not hasattr(cfg, k):
+            raise ValueError(f"unknown rotary constant {k}")
+        setattr(cfg, k, v)
+    f = torch.empty(max(0, int(rope_dim)) // 2, dtype=torch.float64)
+    _check(_lib.fm_rope_frequencies(ctypes.byref(cfg), _ptr(f)), "fm_rope_frequencies")
+    return f if device is None else f.to(device)
+
+
+def fm_kv4_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                  page_table: torch.Tensor, seq: torch.Tensor, pos: torch.Tensor,
+                  inv_freq: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                  q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  k_hat: Optional[torch.Tensor] = None, v_hat: Optional[torch.Tensor] = None,
+                  values: bool = False, stream=None):
+    """Appends T tokens to the 4-bit paged cache: k, v [T, n_kv_heads, 128]
+    (fp32, bf16 or fp16; views of one projection's output are fine), token t
+    to position pos[t] (int64) of row seq[t] (int32; -1: padding).  Keys are
+    rotated by pos (or `positions`) with inv_freq (fm_rope_frequencies: 32 or
+    64 of them; None: no rotation).  q [T, n_q_heads, 128] is rotated into
+    q_out (which may be q).  With `values` (or k_hat, v_hat) the values that
+    the new records stand for come back in bf16, exactly.  Padding leaves its
+    rows of every output as they were (zeros in a new one).
+    k_pages, v_pages: uint8 [n_pages, n_kv_heads, page_size * 68]; page_table:
+    int32 [B, max_pages].  Returns (q_out, k_hat, v_hat)."""
+    cache = _kv4_cache(k_pages, v_pages, page_table)
+    T = k.shape[0]
+    ks, vs = _heads(k, T, "k"), _heads(v, T, "v", k.dtype)
+    if k.shape[1] != k_pages.shape[1] or v.shape[1] != k_pages.shape[1]:
+        raise ValueError("k and v must have the cache's heads")
+    _like(seq, (T,), torch.int32, "seq")
+    _like(pos, (T,), torch.int64, "pos")
+    if positions is not None:
+        _like(positions, (T,), torch.int64, "positions")
+    rope_dim = _check_freq(inv_freq)
+    on = _On(stream, k, v, k_pages, v_pages, page_table, seq, pos, inv_freq, positions, q, q_out, k_hat, v_hat)
+    n_q = qs = qos = 0
+    if q is not None:
+        n_q, qs = q.shape[1], _heads(q, T, "q", k.dtype)
+        if q_out is None:
+            q_out = on.new(torch.zeros, (T, n_q, 128), k.dtype)
+        qos = _heads(q_out, T, "q_out", k.dtype)
+        if q_out.shape[1] != n_q:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if values and k_hat is None:
+        k_hat = on.new(torch.zeros, tuple(k.shape), torch.bfloat16)
+    if values and v_hat is None:
+        v_hat = on.new(torch.zeros, tuple(k.shape), torch.bfloat16)
+    for t, name in ((k_hat, "k_hat"), (v_hat, "v_hat")):
+        if t is not None:
+            _like(t, k.shape, torch.bfloat16, name)
+    if T == 0:
+        return q_out, k_hat, v_hat
+    d = fm_kv4_append_desc(DTYPES[k.dtype], T, n_q, k.data_ptr(), v.data_ptr(), _addr(q), ks, vs, qs, qos,
+                           seq.data_ptr(), pos.data_ptr(), _addr(positions), _addr(inv_freq), rope_dim, _addr(q_out),
+                           _addr(k_hat), _addr(v_hat))
+    with on:
+        _check(_lib.fm_kv4_append(ctypes.byref(cache), ctypes.byref(d), on.stream), "fm_kv4_append")
+    return q_out, k_hat, v_hat
+
+
+def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                     kv_len: torch.Tensor, scale: Optional[float] = None, softcap: float = 0.0,
+                     slopes: Optional[torch.Tensor] = None, window: int = 0,
+                     kv_start: Optional[torch.Tensor] = None, idx: Optional[torch.Tensor] = None,
+                     count: Optional[torch.Tensor] = None, max_len: Optional[int] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of each row's newest tokens over its 4-bit paged cache:
+    q [B, n_q_heads, 128] (one token a row) or [B, Tq, n_q_heads, 128] (the
+    last Tq of the kv_len [B] int32 tokens, causal among themselves), fp32,
+    bf16 or fp16.  scale (128^-1/2), softcap (scores capped by a tanh), slopes
+    [n_q_heads] fp32 (a bias slope * (key position - query position)), window
+    (positions a query sees back, itself included), kv_start [B] int32 (first
+    visible position), idx / count (fm_compact_mask's list: only the kept
+    positions are read).  max_len bounds kv_len where the caller knows it.
+    Returns the output in q's type and shape; 0 for a query that sees nothing."""
+    one = q.dim() == 3
+    if q.dim() not in (3, 4) or q.shape[-1] != 128 or q.dtype not in DTYPES:
+        raise ValueError("q must be [B, heads, 128] or [B, Tq, heads, 128] fp32, bf16 or fp16")
+    B, Tq, n_q = q.shape[0], 1 if one else q.shape[1], q.shape[-2]
+    if q.stride(-1) != 1 or (n_q > 1 and q.stride(-2) != 128):
+        raise ValueError("the heads of a token of q must be packed")
+    if Tq > 1:
+        qs = q.stride(1)
+        if B > 1 and q.stride(0) != Tq * qs:
+            raise ValueError("the tokens of q must be evenly spaced")
+    else:
+        qs = q.stride(0) if B > 1 else n_q * 128
+    cache = _kv4_cache(k_pages, v_pages, page_table)
+    if page_table.shape[0] != B:
+        raise ValueError("page_table must have a row for each of q's")
+    _like(kv_len, (B,), torch.int32, "kv_len")
+    if kv_start is not None:
+        _like(kv_start, (B,), torch.int32, "kv_start")
+    if slopes is not None:
+        _like(slopes, (n_q,), torch.float32, "slopes")
+    max_sel = 0
+    if idx is not None:
+        if idx.dim() != 2 or count is None:
+            raise ValueError("idx must be int32 [B, max_sel], with count")
+        max_sel = idx.shape[1]
+        _like(idx, (B, max_sel), torch.int32, "idx")
+        _like(count, (B,), torch.int32, "count")
+    elif count is not None:
+        raise ValueError("count without idx")
+    on = _On(stream, q, k_pages, v_pages, page_table, kv_len, slopes, kv_start, idx, count, out, workspace)
+    if out is None:
+        out = on.new(torch.empty, tuple(q.shape), q.dtype)
+    _like(out, q.shape, q.dtype, "out")
+    if out.numel() == 0:
+        return out
+    if idx is not None and max_sel == 0:
+        raise ValueError("idx has no entries")
+    bound = cache.max_pages * cache.page_size if max_len is None else int(max_len)
+    d = fm_kv4_attn_desc(DTYPES[q.dtype], Tq, n_q, q.data_ptr(), qs, out.data_ptr(), kv_len.data_ptr(),
+                         _addr(kv_start), bound, _addr(idx), _addr(count), max_sel,
+                         128 ** -0.5 if scale is None else float(scale), float(softcap), _addr(slopes), int(window))
+    rc, rd = ctypes.byref(cache), ctypes.byref(d)
+    if workspace is None:
+        workspace = on.new(torch.empty, (max(16, _lib.fm_kv4_attention_workspace_bytes(rc, rd)),), torch.uint8)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    with on:
+        _check(_lib.fm_kv4_attention(rc, rd, workspace.data_ptr(), workspace.numel(), on.stream), "fm_kv4_attention")
+    return out
+
+
+def fm_index_append(k: torch.Tensor, comp_k: Sequence[torch.Tensor], row: torch.Tensor, chunk: torch.Tensor,
+                    inv_freq: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    hadamard: bool = True, N: Optional[int] = None, stream=None) -> None:
+    """Appends indexer keys as the records that fm_score reads: k [T, L, 128]
+    (fp32, bf16 or fp16), rotated by `positions` (int64 [T]) with inv_freq and
+    Hadamard-transformed, into record chunk[t] of row row[t] (both int32; -1:
+    padding) of each layer's comp_k [B, N_pad, 132] uint8."""
+    T, L = k.shape[0], len(comp_k)
+    ks = _heads(k, T, "k")
+    if L < 1 or k.shape[1] != L:
+        raise ValueError("k must hold a key for each layer of comp_k")
+    B, N_pad, rec = comp_k[0].shape
+    for i, t in enumerate(comp_k):
+        if rec != 132:
+            raise ValueError("compressed keys must be [B, N, 132] uint8")
+        _like(t, (B, N_pad, rec), torch.uint8, f"comp_k[{i}]")
+    _like(row, (T,), torch.int32, "row")
+    _like(chunk, (T,), torch.int32, "chunk")
+    rope_dim = _check_freq(inv_freq)
+    if (inv_freq is None) != (positions is None):
+        raise ValueError("positions and inv_freq belong together")
+    if positions is not None:
+        _like(positions, (T,), torch.int64, "positions")
+    N = N_pad if N is None else int(N)
+    if N > N_pad:
+        raise ValueError("N exceeds the rows of comp_k")
+    on = _On(stream, k, *comp_k, row, chunk, inv_freq, positions)
+    if T == 0 or N == 0 or B == 0:
+        return
+    arr = (ctypes.c_void_p * L)(*[t.data_ptr() for t in comp_k])
+    with on:
+        _check(_lib.fm_index_append(k.data_ptr(), DTYPES[k.dtype], ks, T, L, row.data_ptr(), chunk.data_ptr(),
+                                    _addr(positions), _addr(inv_freq), rope_dim, 1 if hadamard else 0, arr,
+                                    N_pad * 132, B, N, on.stream), "fm_index_append")
+
+
+def fm_add_rmsnorm_fp8(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                       gain: Optional[torch.Tensor] = None, eps: float = 1e-6, group: int = 128,
+                       sum_out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None, stream=None):
+    """z = x + residual; RMSNorm(z) * gain in e4m3 with an fp32 scale for each
+    `group` (128, or H: one a row) elements.  x, residual [T, H] fp32, bf16 or
+    fp16 (rows may be strided).  Returns (z in x's type, codes [T, H]
+    float8_e4m3fn, scales [T, H / group]); sum_out may be x or residual."""
+    if x.dim() != 2 or x.dtype not in DTYPES or x.stride(1) != 1:
+        raise ValueError("x must be [T, H] fp32, bf16 or fp16 with contiguous rows")
+    T, H = x.shape
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.stride(1) != 1):
+        raise ValueError("residual must have x's shape and type")
+    if gain is not None:
+        _like(gain, (H,), x.dtype, "gain")
+    group = int(group)
+    if group < 1 or H % group:
+        raise ValueError("group must be 128 or H")
+    on = _On(stream, x, residual, gain, sum_out, codes, scales)
+    if sum_out is None:
+        sum_out = on.new(torch.empty, (T, H), x.dtype)
+    if codes is None:
+        codes = on.new(torch.empty, (T, H), torch.float8_e4m3fn)
+    if scales is None:
+        scales = on.new(torch.empty, (T, H // group), torch.float32)
+    _like(sum_out, (T, H), x.dtype, "sum_out")
+    _like(codes, (T, H), codes.dtype if codes.dtype == torch.uint8 else torch.float8_e4m3fn, "codes")
+    _like(scales, (T, H // group), torch.float32, "scales")
+    if T == 0:
+        return sum_out, codes, scales
+    rs = 0 if residual is None else residual.stride(0) if T > 1 else H
+    with on:
+        _check(_lib.fm_add_rmsnorm_fp8(x.data_ptr(), x.stride(0) if T > 1 else H, _addr(residual), rs, _addr(gain),
+                                       DTYPES[x.dtype], T, H, float(eps), group, sum_out.data_ptr(), codes.data_ptr(),
+                                       scales.data_ptr(), on.stream), "fm_add_rmsnorm_fp8")
+    return sum_out, codes, scales
 
 
 class Retriever:
