@@ -622,7 +622,7 @@ def test_norm_in_place_strided_and_odd_rows():
     assert torch.isnan(k[1]).all() and torch.isnan(k[2]).all()
     v = c.float().cpu() * k.repeat_interleave(128, dim=1)
     torch.testing.assert_close(v[3], torch.ones(256), rtol=2.0 ** -20, atol=0)
-    assert k[4, 0] == 0 and v[4, 130] == pytest.approx(16.0, rel=2.0 ** -18)
+    assert k[4, 0] == 0 and v[4, 130] == pytest.approx(2.0 / math.sqrt(4.0 / 256 + 1e-6), rel=2.0 ** -18)
 
 
 # -------------------------------------------------------------- a run of them
