@@ -545,9 +545,10 @@ fm_status fm_kv4_append(const fm_kv4_cache* cache, const fm_kv4_append_desc* d, 
  * A query that sees nothing gives 0 (kv_len 0, a position below 0, an empty
  * window or list).  What a query does not see is not touched by it, whatever
  * its records hold.  Query head h uses kv head h / (n_q_heads / n_kv_heads).
- * Dot products, statistics and sums are fp32; fp32 queries and the softmax
- * weights enter the products at 2^-22 or better, 16-bit ones exactly, their
- * weights at 2^-11. */
+ * Dot products, statistics and sums are fp32.  The products' operands are f16:
+ * 16-bit queries enter exactly and their weights at 2^-11, fp32 queries and
+ * their weights in two pieces at 2^-22; a weight below 2^-22 of the largest has
+ * an absolute step of 2^-33 of that. */
 typedef struct fm_kv4_attn_desc {
   int dtype;                  /* FM_F32, FM_BF16, FM_F16: of q and out */
   int Tq;                     /* query tokens of every row, 1..64 */

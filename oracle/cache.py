@@ -103,9 +103,11 @@ def read_cache(pages: np.ndarray, page_table: np.ndarray, page_size: int):
 def attention(q, k, v, there, kv_len, scale=None, softcap=0.0, slopes=None, window=0, kv_start=None, idx=None,
               count=None):
     """q [B, Tq, Hq, 128]; k, v [B, Hkv, n, 128] fp64; there [B, n].  Returns
-    (out, err_x, abs_v): the output, the largest |scale| * sum |q||k| + |x| over what a
-    query sees (what a logit's rounding error scales with), and sum p |v|
-    (what the output's scales with), each [B, Tq, Hq, 128 or 1]."""
+    (out, err_x, abs_v, top_v): the output; what a logit's rounding error
+    scales with, the largest |scale| * (sum |q||k| + sum |q| * max |k| / 16) + |x|
+    over what a query sees; what the output's scales with, sum p |v|; and what
+    the smallest weights' and values' absolute steps scale with,
+    2^-33 * 12 n max(p max|v|) + 2^-24 sum p max|v|; each [B, Tq, Hq, 128 or 1]."""
     q = np.asarray(q, np.float64)
     B, Tq, Hq, _ = q.shape
     Hkv = k.shape[1]
@@ -113,6 +115,7 @@ def attention(q, k, v, there, kv_len, scale=None, softcap=0.0, slopes=None, wind
     out = np.zeros(q.shape)
     abs_v = np.zeros(q.shape)
     err_x = np.zeros((B, Tq, Hq, 1))
+    top_v = np.zeros((B, Tq, Hq, 1))
     for b in range(B):
         n = int(min(max(kv_len[b], 0), there.shape[1]))
         lo = max(0, int(kv_start[b])) if kv_start is not None else 0
@@ -133,7 +136,8 @@ def attention(q, k, v, there, kv_len, scale=None, softcap=0.0, slopes=None, wind
             for h in range(Hq):
                 kh = h // (Hq // Hkv)
                 x = scale * (k[b, kh, j] @ q[b, t, h])
-                e = abs(scale) * (np.abs(k[b, kh, j]) @ np.abs(q[b, t, h]))
+                e = abs(scale) * (np.abs(k[b, kh, j]) @ np.abs(q[b, t, h])
+                                  + np.abs(q[b, t, h]).sum() * np.abs(k[b, kh, j]).max(axis=1) / 16)
                 if softcap > 0:
                     x = softcap * np.tanh(x / softcap)
                     e = e + softcap
@@ -145,7 +149,9 @@ def attention(q, k, v, there, kv_len, scale=None, softcap=0.0, slopes=None, wind
                 out[b, t, h] = w @ v[b, kh, j]
                 abs_v[b, t, h] = w @ np.abs(v[b, kh, j])
                 err_x[b, t, h] = (e + np.abs(x)).max()
-    return out, err_x, abs_v
+                pv = w * np.abs(v[b, kh, j]).max(axis=1)
+                top_v[b, t, h] = 2.0 ** -33 * 12 * j.size * pv.max() + 2.0 ** -24 * pv.sum()
+    return out, err_x, abs_v, top_v
 
 
 # --------------------------------------------------- indexer keys and the norm

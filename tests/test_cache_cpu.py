@@ -239,14 +239,14 @@ def test_oracle_attention_reduces_to_plain_cases():
     k, v = r.standard_normal((1, 1, 5, 128)), r.standard_normal((1, 1, 5, 128))
     there = np.ones((1, 5), bool)
     zero = np.zeros((1, 1, 1, 128))
-    o, _, _ = OC.attention(zero, k, v, there, [5])
+    o, *_ = OC.attention(zero, k, v, there, [5])
     np.testing.assert_allclose(o[0, 0, 0], v[0, 0].mean(0))
-    o, _, _ = OC.attention(zero, k, v, there, [5], window=2)
+    o, *_ = OC.attention(zero, k, v, there, [5], window=2)
     np.testing.assert_allclose(o[0, 0, 0], v[0, 0, 3:].mean(0))
-    o, _, _ = OC.attention(zero, k, v, there, [5], idx=np.array([[4, 9, -1, 0]]), count=[4])
+    o, *_ = OC.attention(zero, k, v, there, [5], idx=np.array([[4, 9, -1, 0]]), count=[4])
     np.testing.assert_allclose(o[0, 0, 0], (v[0, 0, 4] + v[0, 0, 0]) / 2)
-    o, _, _ = OC.attention(zero, k, v, there, [5], slopes=[1000.0])
+    o, *_ = OC.attention(zero, k, v, there, [5], slopes=[1000.0])
     np.testing.assert_allclose(o[0, 0, 0], v[0, 0, 4])
-    o, _, _ = OC.attention(np.zeros((1, 3, 1, 128)), k, v, there, [2])
+    o, *_ = OC.attention(np.zeros((1, 3, 1, 128)), k, v, there, [2])
     assert not o[0, 0].any()  # the first of three queries stands before the row's start
     np.testing.assert_allclose(o[0, 1, 0], v[0, 0, 0])

@@ -5,11 +5,21 @@ records, the residual RMSNorm, and a run of them together with the retriever.
 
 Tolerances.  Stored codes are equal, bit for bit.  An attention output is off
 by at most
-    (2 dx + w) * sum p|v| + eps/2 * |o|
+    (2 dx + w) * sum p|v| + small + eps/2 * |o|
 with dx the error of a logit: 2^-20 of what its terms and its cap and bias add
 up to (fp32 products summed in fp32, queries split to 2^-22, exp2 and tanh to a
 few 2^-23 each), w the weights' rounding (2^-11 for 16-bit types, 2^-20 for
-fp32, and 2^-23 for each sixteen tokens summed), eps the output type's step."""
+fp32, and 2^-23 for each sixteen tokens summed), eps the output type's step.
+
+`small` is what the f16 operands' subnormals cost.  Weights are held times 2^8
+relative to the largest p * (size of v), where a record's size is its largest
+scale; the steps of f16 end at 2^-24, so a weight is off by up to 2^-25 * 2^-8 =
+2^-33 of the largest, and each of n tokens adds that times its largest code, 6
+(6 sizes are at most 12 times the record's largest |v|: some code of the
+largest group is at least 1/2).  A value far below its record's size is off by
+2^-25 sizes, at most 2^-24 times the record's largest |v|, weighted by p; a key
+element likewise, which adds |q| times 2^-24 max|k| to a logit (in dx, as
+2^-20 / 16)."""
 import math
 
 import numpy as np
@@ -56,13 +66,13 @@ def check_attention(o, q, kp, vp, table, lens, page, **kw):
     v, _ = OC.read_cache(vp, table, page)
     Tq = q.shape[1]
     with np.errstate(all="ignore"):
-        ref, err_x, abs_v = OC.attention(q.double().numpy(), k, v, there, lens, **kw)
+        ref, err_x, abs_v, top_v = OC.attention(q.double().numpy(), k, v, there, lens, **kw)
     narrow = o.dtype != torch.float32
     n = max(1, k.shape[2])
     w = (2.0 ** -11 if narrow else 2.0 ** -20) + 2.0 ** -23 * (n / 16 + 16)
     # below the type's smallest normal number (2^-14 in fp16) its steps are tiny * eps apart, whatever the value
     sub = torch.finfo(o.dtype).tiny * half_step(o.dtype) + 1e-37
-    tol = (2 * 2.0 ** -20 * err_x + w) * abs_v + half_step(o.dtype) * np.abs(ref) + sub
+    tol = (2 * 2.0 ** -20 * err_x + w) * abs_v + top_v + half_step(o.dtype) * np.abs(ref) + sub
     got = o.double().cpu().numpy().reshape(ref.shape)
     bad = np.abs(got - ref) > tol
     assert np.isfinite(got).all() and not bad.any(), (
@@ -363,10 +373,34 @@ def test_attention_a_seen_nan_makes_its_rows_nan_only():
         q = torch.from_numpy(rng.standard_normal((2, 4, 128))).bfloat16().to(DEV)
         o = fm.fm_kv4_attention(q, dev(kp), dev(vp), dev(table), dev(np.array(lens, np.int32))).float().cpu()
         if which == 0:
-            assert torch.isnan(o[0, :2]).all()
+            assert torch.isnan(o[0, :2]).all()  # a logit is NaN: so is its softmax
         else:
             assert torch.isnan(o[0, :2, 64:96]).all()
         assert torch.isfinite(o[0, 2:]).all() and torch.isfinite(o[1]).all()
+
+
+def test_attention_a_nan_reaches_the_queries_that_see_it_only():
+    """Drafts, a window and starts: the NaN record lies before, among or after
+    what a query sees."""
+    rng = np.random.default_rng(16)
+    lens, page, Tq = [60, 61], 16, 4
+    kp, vp, table = make_cache(rng, lens, 1, page)
+    q = torch.from_numpy(rng.standard_normal((2, Tq, 2, 128))).half().to(DEV)
+    for at in (30, 57, 59):
+        for p in (kp, vp):
+            x = p.copy()
+            x[table[0, at // 16], 0, page * 64 + 4 * (at % 16)] = 255  # row 0: dims 0..31
+            pools = (x, vp) if p is kp else (kp, x)
+            for kw in (dict(), dict(window=2), dict(window=28)):
+                o = fm.fm_kv4_attention(q, dev(pools[0]), dev(pools[1]), dev(table), dev(np.array(lens, np.int32)),
+                                        **kw).float().cpu()
+                assert torch.isfinite(o[1]).all()
+                for t in range(Tq):
+                    pos = 60 - Tq + t
+                    sees = at <= pos and pos - at < kw.get("window", 1 << 30)
+                    assert bool(torch.isnan(o[0, t, :, :32]).all()) == sees, (at, kw, t)
+                    if not sees:
+                        assert torch.isfinite(o[0, t]).all()
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
@@ -682,9 +716,9 @@ def test_a_decode_step_from_the_hidden_state_to_the_output():
             for b in range(B):
                 k[b, :, :lens[b]] = np.stack(store_k[b], 1)
                 v[b, :, :lens[b]] = np.stack(store_v[b], 1)
-            ref, err_x, abs_v = OC.attention(q.double().cpu().numpy()[:, None], k, v, np.ones((B, N), bool), lens,
+            ref, err_x, abs_v, top_v = OC.attention(q.double().cpu().numpy()[:, None], k, v, np.ones((B, N), bool), lens,
                                              softcap=40.0, idx=idx.cpu().numpy(), count=count.cpu().numpy())
-            tol = (2 * 2.0 ** -20 * err_x + 2.0 ** -11 + 2.0 ** -18) * abs_v + 2.0 ** -8 * np.abs(ref)
+            tol = (2 * 2.0 ** -20 * err_x + 2.0 ** -11 + 2.0 ** -18) * abs_v + top_v + 2.0 ** -8 * np.abs(ref)
             assert (np.abs(o.double().cpu().numpy()[:, None] - ref) <= tol).all()
     finally:
         r.close()
