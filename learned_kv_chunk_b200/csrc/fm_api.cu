@@ -446,7 +446,8 @@ fm_status fm_sync_status(fm_ctx* c, cudaStream_t stream) {
   }
   const bool attn = take_attention_error() != kDevErrNone;
   const bool recall = take_recall_error() != kDevErrNone;
-  if (attn || recall) return FM_ERR_DEVICE;
+  const bool kv4 = take_kv4_error() != kDevErrNone;
+  if (attn || recall || kv4) return FM_ERR_DEVICE;
   return FM_OK;
 }
 

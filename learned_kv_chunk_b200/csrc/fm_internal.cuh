@@ -180,6 +180,8 @@ fm_status launch_topk_shard_mask(const float* ens, int B, int N, const int32_t* 
 int take_attention_error();
 // The same for the recall kernels' bulk-copy waits (compaction and gather).
 int take_recall_error();
+// The same for the waits of the attention over the 4-bit cache.
+int take_kv4_error();
 
 #if defined(__CUDACC__)
 

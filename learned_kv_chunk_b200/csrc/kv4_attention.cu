@@ -1,6 +1,7 @@
 // kv4_attention.cu -- attention over the 4-bit paged cache (fm_kv4_attention).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -23,19 +24,46 @@ struct AttnArgs {
   int Tq, n_q, max_len, max_sel, window;
   float coef, softcap, cap_log2;
   uint32_t page_magic;  // ceil(2^32 / (page_size / 16)), 0 for a page of 16
-  int row_tiles, chunk, splits;
-  float* part_o;        // [B * Tq * n_q, splits, 128]
-  float2* part_ml;      // [B * Tq * n_q, splits]: the maximum (log2 units), the sum
+  int row_tiles;
+  int run;              // tokens that lie together wherever they are: the largest power of two in a page
+  // the partial results of units that several CTAs share: two slots a CTA, its first segment's and its last's
+  struct Share* share;  // [CTAs]
+  float2* part_ml;      // [CTAs][2][rows of a tile]: the maximum (log2 units), the sum
+  float* part_o;        // [CTAs][2][rows of a tile][128]
 };
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTok = 32;                  // tokens a warp takes at a time
-constexpr int kBlockTok = kTok * kWarps;  // tokens a CTA takes at a time
+// What a CTA says of the unit in which its range begins, if it is the second
+// of those that share it: where the parts are.
+struct Share {
+  int b, unit;       // row (-1: nothing to merge), kv head * row_tiles + row tile
+  int parts, slot0;  // parts: those of the CTA before this one (at slot0), of this one and of the next ones
+};
+
+// A CTA has consumer warps and a producer warp, together a multiple of what fills
+// the four schedulers' register files: 16 warps of 128 registers an SM where 8
+// rows suffice, 12 of 168 for 16 rows or two pieces, 8 of 255 for 32 rows.  A
+// stage holds a block of tokens: a tile (16 tokens, or twice 16) for each
+// consumer.
+constexpr int kMaxRunTok = 32;
+template <int NT, int P>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kHalves = NT == 4 ? 1 : 2;      // 16-token halves of a tile: 32 rows leave registers for one
+  static constexpr int kTok = 16 * kHalves;
+  static constexpr int kWarps = NT == 4 || (NT == 1 && P == 1) ? 7 : 5;  // consumers
+  static constexpr int kBlock = kWarps * kTok;         // tokens of a stage, the unit in which work is shared out
+  static constexpr int kCtas = NT == 4 ? 1 : 2;        // that an SM holds
+  static constexpr int kStages = NT == 4 ? 6 : 3;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kMergers = 3;                   // the most warps that add to others at once
+};
+constexpr int block_tokens(int nt, int pieces) { return nt == 4 ? 112 : nt == 1 && pieces == 1 ? 224 : 160; }
+constexpr int ctas_per_sm(int nt) { return nt == 4 ? 1 : 2; }
+
 constexpr float kNoMax = -1e30f;          // the running maximum of a row that has seen nothing
 constexpr float kLazy = 6.f;              // the maximum may be exceeded by 2^6 before the sums are rescaled
 constexpr float kLift = 8.f;              // weights are held times 2^8: at most 2^14 in f16
-constexpr int kORow = 132;                // floats between rows of the warps' outputs in shared memory
+constexpr int kORow = 132;         // floats between rows of the warps' outputs in shared memory
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -80,65 +108,65 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-__device__ __forceinline__ uint4 ldg128(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ldg64(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Arrives on `bar` once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// What a warp keeps of the tokens it is at, written by one lane a token.
-struct TokenInfo {
-  float k_factor;   // 2^r of the key's largest scale r; the groups' factors are relative to it
-  float v_exp;      // log2 of the value's
-  float v_inv;      // 2^-v_exp
-  int pos;          // position, -1 where there is none
-  uint16_t kf[4];   // f16 factors of the key's groups, 2^(scale - r)
-  uint16_t vf[4];   // and of the value's
+__device__ int g_kv4_err;  // kDevErrTimeout once a wait of the attention's ran out
+
+// The factors of a record's groups.  A tile whose scale bytes all lie in
+// [113, 139] (2^-14 .. 2^12: what real keys and values have) is FAST: a group's
+// factor is the f16 number of that exponent, (byte - 112) << 10, and its
+// products with a code are exact.  Any other tile takes the general form: each
+// record's factors are relative to its largest scale 2^r, which multiplies the
+// score (keys) or joins the weight's exponent (values).
+__device__ __forceinline__ bool fast_scales(uint32_t w) {
+  // bytes + 116 in [224, 255] is [108, 139], + 15 in [128, 255] is [113, 240]; a
+  // byte that carries into its neighbour fails the first test itself
+  return (((w + 0x74747474u) & 0xe0e0e0e0u) == 0xe0e0e0e0u) && (((w + 0x0f0f0f0fu) & 0x80808080u) == 0x80808080u);
+}
+// Two f16 factors from the bytes 0 and 2 of p (bytes 1 and 3 are 0).
+__device__ __forceinline__ uint32_t fast_factor(uint32_t p) { return p * 1024u - 112u * 1024u * 65537u; }
+
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 255u; }
+__device__ __forceinline__ bool has_nan(uint32_t w) {
+  return byte_of(w, 0) == 255u || byte_of(w, 1) == 255u || byte_of(w, 2) == 255u || byte_of(w, 3) == 255u;
+}
+// The largest scale byte that is not NaN.
+__device__ __forceinline__ uint32_t top_scale(uint32_t w) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r = max(r, byte_of(w, i) == 255u ? 0u : byte_of(w, i));
+  return r;
+}
+// A value's size: a record of zeros has none of its own, below 2^-100 none is kept.
+__device__ __forceinline__ uint32_t top_value_scale(uint32_t w) {
+  const uint32_t r = top_scale(w);
+  return r == 0u ? 127u : max(r, 27u);
+}
+// f16 bits of 2^(byte i - r), 0 below 2^-25.
+__device__ __forceinline__ uint32_t group_factor(uint32_t w, int i, uint32_t r) {
+  const __half h = __float2half_rn(__int_as_float(max(127 + (int)byte_of(w, i) - (int)r, 0) << 23));
+  return __half_as_ushort(h);
+}
+
+// A block in shared memory.
+template <int BLOCK>
+struct alignas(128) Stage {
+  uint8_t k[BLOCK * kKvCodeBytes], v[BLOCK * kKvCodeBytes];
+  uint32_t ks[BLOCK], vs[BLOCK];
+  int pos[BLOCK];   // list: the entries' positions, -1: none
+  uint32_t there;   // no list: bit i, tokens 16i .. 16i + 15 are there
 };
 
-__device__ __forceinline__ uint32_t max_byte(uint32_t w) {
-  w = __vmaxu4(w, w >> 16);
-  w = __vmaxu4(w, w >> 8);
-  return w & 255u;
-}
-
-// f16 2^(byte - r) for r >= byte (0 below 2^-24).
-__device__ __forceinline__ uint32_t group_factors(uint32_t w, int shift, uint32_t r) {
-  const int e0 = 127 + (int)((w >> shift) & 255u) - (int)r, e1 = 127 + (int)((w >> (shift + 8)) & 255u) - (int)r;
-  return pack_f16(__int_as_float(max(e0, 0) << 23), __int_as_float(max(e1, 0) << 23));
-}
-
-// Fills in a token's info; returns whether a scale of its value is NaN (the
-// group's factor is then the f16 NaN 0x7fff, which no product may use).
-__device__ __forceinline__ bool write_token(TokenInfo* ti, uint32_t kw, uint32_t vw, int pos) {
-  if (pos < 0) kw = vw = 0u;
-  const uint32_t kn = __vcmpeq4(kw, 0xffffffffu), vn = __vcmpeq4(vw, 0xffffffffu);  // NaN scales
-  const uint32_t ks = kw & ~kn, vs = vw & ~vn;
-  const uint32_t rk = max_byte(ks);
-  uint32_t rv = max_byte(vs);
-  rv = rv == 0u ? 127u : max(rv, 27u);  // a value of zeros has no size of its own; below 2^-100 none is kept
-  TokenInfo t;
-  t.k_factor = kn ? nan_f32() : __uint_as_float(rk ? rk << 23 : 0x00400000u);
-  t.v_exp = (float)((int)rv - 127);
-  t.v_inv = __uint_as_float(rv < 254u ? (254u - rv) << 23 : 0x00400000u);
-  t.pos = pos;
-  uint32_t f[4] = {group_factors(ks, 0, rk), group_factors(ks, 16, rk), group_factors(vs, 0, rv),
-                   group_factors(vs, 16, rv)};
-  if (vn) {
-    f[2] |= __byte_perm(vn, 0, 0x1100) & 0x7fff7fffu;
-    f[3] |= __byte_perm(vn, 0, 0x3322) & 0x7fff7fffu;
-  }
-  reinterpret_cast<uint4*>(ti)[0] = make_uint4(__float_as_uint(t.k_factor), __float_as_uint(t.v_exp),
-                                               __float_as_uint(t.v_inv), (uint32_t)t.pos);
-  reinterpret_cast<uint4*>(ti)[1] = make_uint4(f[0], f[1], f[2], f[3]);
-  return vn != 0u;
-}
+constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
 
 // x / 16 / (page_size / 16) for x < 2^30: the page of a position.
 __device__ __forceinline__ int page_index(const AttnArgs& a, int pos) {
@@ -146,284 +174,449 @@ __device__ __forceinline__ int page_index(const AttnArgs& a, int pos) {
   return a.page_magic ? (int)__umulhi(x, a.page_magic) : (int)x;
 }
 
-template <class T, int NT, int P, bool LIST>
-__global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const AttnArgs a) {
-  constexpr int kRows = 8 * NT;
-  constexpr bool kQReg = NT == 1;
-  extern __shared__ __align__(16) uint8_t smem[];
-  // [token infos of the warps][queries, when they are not kept in registers]; at the end the warps' outputs
-  TokenInfo* info = reinterpret_cast<TokenInfo*>(smem) + (threadIdx.x >> 5) * kTok;
-  uint2* sq = reinterpret_cast<uint2*>(smem + kWarps * kTok * sizeof(TokenInfo));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.z, split = blockIdx.x;
-  const int kh = blockIdx.y / a.row_tiles, r0 = (blockIdx.y - kh * a.row_tiles) * kRows;
-  const int G = a.n_q / a.c.n_heads, rows = min(kRows, a.Tq * G - r0);
-  const int len = max(0, min(__ldg(a.kv_len + b), a.max_len));
-  const int start = a.kv_start ? max(0, __ldg(a.kv_start + b)) : 0;
-  const int p_first = len - a.Tq + r0 / G, p_last = len - a.Tq + (r0 + rows - 1) / G;
-  const auto low_of = [&](int p) { return a.window > 0 ? max(start, p - a.window + 1) : start; };
-  const int lo_first = low_of(p_first), lo_last = low_of(p_last);
-  // this CTA's tokens (list entries): [n0, n1)
-  int n0, n1;
+// What a row holds: its length and first visible position, its tokens (list
+// entries) [from, to), cut into blocks; one block even if it has none, for its
+// output.
+struct Range {
+  int len, start, from, to, blocks;
+};
+template <int BLOCK, bool LIST>
+__device__ __forceinline__ Range row_range(const AttnArgs& a, int b) {
+  Range r;
+  r.len = max(0, min(__ldg(a.kv_len + b), a.max_len));
+  r.start = a.kv_start ? max(0, __ldg(a.kv_start + b)) : 0;
   if (LIST) {
-    n0 = split * a.chunk;
-    n1 = min(n0 + a.chunk, max(0, min(__ldg(a.count + b), a.max_sel)));
-    if (p_last < 0) n1 = 0;
+    r.from = 0;
+    r.to = max(0, min(__ldg(a.count + b), a.max_sel));
   } else {
-    n0 = (lo_first & ~(kTok - 1)) + split * a.chunk;
-    n1 = min(n0 + a.chunk, p_last + 1);
+    const int p = r.len - a.Tq;  // the first query's position
+    r.from = (a.window > 0 ? max(r.start, p - a.window + 1) : r.start) & ~(kMaxRunTok - 1);
+    r.to = r.len;
   }
-  const auto part_row = [&](int r) {  // the row's place among [B, Tq, n_q]
-    const int tq = (r0 + r) / G;
-    return ((int64_t)b * a.Tq + tq) * a.n_q + kh * G + (r0 + r - tq * G);
-  };
-  if (n0 >= n1) {  // nothing here
-    if (a.splits > 1) {
-      if ((int)threadIdx.x < rows)
-        a.part_ml[part_row(threadIdx.x) * a.splits + split] = make_float2(-INFINITY, 0.f);
-    } else {
-      for (int i = threadIdx.x; i < rows * kKvDim; i += kThreads)
-        store1(static_cast<T*>(a.out) + part_row(i / kKvDim) * kKvDim + i % kKvDim, 0.f);
+  r.blocks = max(1, (r.to - r.from + BLOCK - 1) / BLOCK);
+  return r;
+}
+
+// The place of query row r (token r / G, head r % G of the kv head) among [B, Tq, n_q].
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, int b, int kh, int G, int r) {
+  const int tq = r / G;
+  return ((int64_t)b * a.Tq + tq) * a.n_q + kh * G + (r - tq * G);
+}
+
+__device__ __forceinline__ uint64_t div_small(uint64_t x, uint64_t y) {
+  return ((x | y) >> 32) == 0 ? (uint32_t)x / (uint32_t)y : x / y;
+}
+
+template <int N>
+__device__ __forceinline__ void named_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+
+// The walk over a CTA's blocks: segments of units (a row's kv head and tile of
+// query rows), in the same order for the producer and the consumers.
+template <int BLOCK, bool LIST>
+struct Walk {
+  int64_t w, end, base;  // next block, the range's end, blocks of the rows before b (for one unit)
+  int b, units;
+  Range rg;
+  // the current segment
+  int unit, i0, i1;
+  __device__ __forceinline__ void segment() {
+    const int64_t x = w - base * units;
+    unit = (int)div_small(x, rg.blocks);
+    i0 = (int)(x - (int64_t)unit * rg.blocks);
+    i1 = (int)min((int64_t)rg.blocks, i0 + (end - w));
+  }
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    w += i1 - i0;
+    if (w < end && w == (base + rg.blocks) * units) {  // the next row
+      base += rg.blocks;
+      rg = row_range<BLOCK, LIST>(a, ++b);
     }
+  }
+};
+
+template <class T, int NT, int P, bool LIST>
+__global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) kv4_attn_kernel(const AttnArgs a) {
+  using S = Shape<NT, P>;
+  constexpr int kRows = S::kRows, H = S::kHalves, kTok = S::kTok, kBlock = S::kBlock, kWarps = S::kWarps;
+  constexpr int kStages = S::kStages;
+  constexpr bool kQReg = NT == 1;
+  using St = Stage<kBlock>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  St* stages = reinterpret_cast<St*>(smem);
+  // the queries, when they are not kept in registers, then the merge's outputs of half of the warps
+  uint2* sq = reinterpret_cast<uint2*>(stages + kStages);
+  float* so = reinterpret_cast<float*>(sq + (kQReg ? 0 : NT * P * 8 * 32));
+  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ int64_t sums[kWarps + 1], found[2];
+  __shared__ float2 sml[S::kMergers][kRows];
+  __shared__ int abort_flag;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.n_q / a.c.n_heads;
+
+  // ---- this CTA's share of the work
+  Walk<kBlock, LIST> wk;
+  wk.units = a.c.n_heads * a.row_tiles;
+  {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&full[i], LIST ? 64 : 1);
+        mbar_init(&empty[i], kWarps);
+      }
+      abort_flag = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // rows in order, `per` a thread
+    const int per = (a.c.B + S::kThreads - 1) / S::kThreads, first = threadIdx.x * per;
+    int64_t mine = 0;
+    for (int i = first; i < min(first + per, a.c.B); ++i) mine += row_range<kBlock, LIST>(a, i).blocks;
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps + 1; ++i) {
+      if (i < warp) upto += sums[i];
+      total += sums[i];
+    }
+    total *= wk.units;
+    const int64_t n_cta = min((int64_t)gridDim.x, total);
+    if (blockIdx.x >= n_cta) {
+      if (threadIdx.x == 0) a.share[blockIdx.x].b = -1;
+      return;
+    }
+    wk.w = div_small(total * blockIdx.x, n_cta);
+    wk.end = div_small(total * (blockIdx.x + 1), n_cta);
+    int64_t before = upto - mine;
+    if (wk.w >= before * wk.units && wk.w < upto * wk.units) {
+      int i = first;
+      for (;; ++i) {
+        const int nb = row_range<kBlock, LIST>(a, i).blocks;
+        if (wk.w < (before + nb) * wk.units) break;
+        before += nb;
+      }
+      found[0] = i;
+      found[1] = before;
+    }
+    __syncthreads();
+    wk.b = (int)found[0];
+    wk.base = found[1];
+    wk.rg = row_range<kBlock, LIST>(a, wk.b);
+    wk.segment();
+    if (threadIdx.x == 0) {
+      // the CTAs c with total * c / n_cta <= x own block x: the last of them is ((x + 1) * n_cta - 1) / total
+      Share sh = {-1, wk.unit, 0, 0};
+      const int64_t w0 = wk.w - wk.i0, w1 = w0 + wk.rg.blocks;
+      const int64_t prev = blockIdx.x ? (int64_t)div_small(total * (blockIdx.x - 1), n_cta) : 0;
+      if (wk.i0 > 0 && prev <= w0) {
+        sh.b = wk.b;
+        sh.parts = (int)div_small(w1 * n_cta - 1, total) - (int)blockIdx.x + 2;
+        sh.slot0 = 2 * ((int)blockIdx.x - 1) + (w0 > prev ? 1 : 0);
+      }
+      a.share[blockIdx.x] = sh;
+    }
+  }
+
+  int stage = 0;
+  uint32_t phase = 0;
+  const auto advance = [&] {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+
+  if (warp == kWarps) {
+    // ---- the producer: a stage for every block, as soon as the consumers have left it
+    const int scales_at = a.c.page_size * kKvCodeBytes;
+    bool ok = true;
+    uint32_t filled = 0;  // stages whose copies are under way
+    for (; ok && wk.w < wk.end; wk.next(a), wk.segment()) {
+      const int kh = wk.unit / a.row_tiles;
+      const int32_t* table = a.c.table + wk.b * a.c.table_stride;
+      const uint8_t* kp = a.c.k + kh * a.c.head_stride;
+      const uint8_t* vp = a.c.v + kh * a.c.head_stride;
+      for (int i = wk.i0; i < wk.i1; ++i) {
+        const int n = wk.rg.from + i * kBlock;
+        St& st = stages[stage];
+        if constexpr (LIST) {
+          constexpr int kPer = (kBlock + 31) / 32;
+          int pos[kPer], page[kPer], slot[kPer];  // of entries lane + 32e
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const int x = n + 32 * e + lane;
+            pos[e] = 32 * e + lane < kBlock && x < wk.rg.to ? __ldg(a.idx + (int64_t)wk.b * a.max_sel + x) : -1;
+            if (pos[e] < 0 || pos[e] >= wk.rg.len) pos[e] = -1;
+          }
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const int pg = pos[e] >= 0 ? page_index(a, pos[e]) : 0;
+            slot[e] = pos[e] - pg * a.c.page_size;
+            page[e] = pos[e] >= 0 ? __ldg(table + pg) : -1;
+            if (page[e] < 0 || page[e] >= a.c.n_pages) page[e] = pos[e] = -1;
+          }
+          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, &abort_flag, &g_kv4_err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const int64_t blk = max(page[e], 0) * a.c.page_stride;
+            const int64_t off = pos[e] >= 0 ? blk + slot[e] * kKvCodeBytes : -1;
+            if (32 * e + lane < kBlock) st.pos[32 * e + lane] = pos[e];
+            if (pos[e] >= 0) {
+              cp_async4(&st.ks[32 * e + lane], kp + blk + scales_at + slot[e] * kKvScaleBytes);
+              cp_async4(&st.vs[32 * e + lane], vp + blk + scales_at + slot[e] * kKvScaleBytes);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {  // four lanes an entry's 64 bytes
+              const int x = 8 * r + (lane >> 2);
+              const int64_t o = __shfl_sync(0xffffffffu, off, x);
+              if (o < 0) continue;
+              cp_async16(st.k + (32 * e + x) * kKvCodeBytes + 16 * (lane & 3), kp + o + 16 * (lane & 3));
+              cp_async16(st.v + (32 * e + x) * kKvCodeBytes + 16 * (lane & 3), vp + o + 16 * (lane & 3));
+            }
+          }
+          cp_async_arrive(&full[stage]);
+          mbar_arrive(&full[stage]);
+        } else {
+          // `run` tokens of a page lie together: a lane a run
+          const int at = n + lane * a.run;
+          const bool in = lane * a.run < kBlock && at < wk.rg.to;
+          const int pg = in ? page_index(a, at) : 0;
+          const int page = in ? __ldg(table + pg) : -1;
+          const int slot = at - pg * a.c.page_size;
+          const bool there = page >= 0 && page < a.c.n_pages;
+          const uint32_t runs = __ballot_sync(0xffffffffu, there);
+          const uint32_t chunks = __ballot_sync(0xffffffffu, lane * 16 < kBlock && ((runs >> (lane * 16 / a.run)) & 1u));
+          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, &abort_flag, &g_kv4_err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            st.there = chunks;
+            mbar_arrive_expect_tx(&full[stage], (uint32_t)__popc(runs) * a.run * kKvBytes * 2);
+          }
+          __syncwarp();
+          if (there) {
+            const int64_t blk = page * a.c.page_stride;
+            const int to = lane * a.run;
+            bulk_g2s(st.k + to * kKvCodeBytes, kp + blk + slot * kKvCodeBytes, a.run * kKvCodeBytes, &full[stage]);
+            bulk_g2s(st.v + to * kKvCodeBytes, vp + blk + slot * kKvCodeBytes, a.run * kKvCodeBytes, &full[stage]);
+            bulk_g2s(st.ks + to, kp + blk + scales_at + slot * kKvScaleBytes, a.run * kKvScaleBytes, &full[stage]);
+            bulk_g2s(st.vs + to, vp + blk + scales_at + slot * kKvScaleBytes, a.run * kKvScaleBytes, &full[stage]);
+          }
+        }
+        filled |= 1u << stage;
+        advance();
+      }
+      if (!ok) break;
+    }
+    // copies may be under way only if a wait ran out: they land before the CTA ends
+    if (!ok)
+      for (int i = 0; i < kStages; ++i) {
+        const bool wrapped = i < stage;  // filled in this round
+        if ((filled >> i) & 1u) mbar_drain(&full[i], wrapped ? phase : phase ^ 1, &g_kv4_err);
+      }
     return;
   }
 
-  // the queries: row g of each tile, dims 32t .. 32t+31, as f16 pieces of q * 2^-e, |.| < 2^8
-  uint32_t qf[kQReg ? P : 1][8][2];
-  float coef[NT][2];            // of columns 2t, 2t + 1: scale * 2^e (* log2 e without a cap)
-  float slope[NT][2];
-  int pq[NT][2];
+  // ---- the consumers
+  const int g = lane >> 2, t = lane & 3;
+  const int tk = (g >> 1) + 4 * (g & 1);  // the token of key row g (row g + 8: + 8)
+  const int grp = g >> 1;                 // the scale group of dims 16g ..
+  int slot = 0;                           // of the segment's partial result
+  bool ok = true;
+  for (; wk.w < wk.end; wk.next(a), wk.segment()) {
+    const Range& rg = wk.rg;
+    const bool complete = wk.i0 == 0 && wk.i1 == rg.blocks;
+    const int kh = wk.unit / a.row_tiles, r0 = (wk.unit - kh * a.row_tiles) * kRows;
+    const int rows = min(kRows, a.Tq * G - r0), len = rg.len;
+    const int p_first = len - a.Tq + r0 / G, p_last = len - a.Tq + (r0 + rows - 1) / G;
+    const auto low_of = [&](int p) { return a.window > 0 ? max(rg.start, p - a.window + 1) : rg.start; };
+    const int lo_last = low_of(p_last);
+
+    // the queries: row g of each tile, dims 32t .. 32t+31, as f16 pieces of q * 2^-e, |.| < 2^8
+    uint32_t qf[kQReg ? P : 1][8][2];
+    float coef[NT][2];            // of columns 2t, 2t + 1: scale * 2^e (* log2 e without a cap)
+    float slope[NT][2];
+    int pq[NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    float v[32];
-    if (r < rows) {
-      const int tq = (r0 + r) / G;
-      const T* q = static_cast<const T*>(a.q) + ((int64_t)b * a.Tq + tq) * a.q_stride +
-                   (kh * G + (r0 + r - tq * G)) * kKvDim + 32 * t;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      float v[32];
+      if (r < rows) {
+        const int tq = (r0 + r) / G;
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)wk.b * a.Tq + tq) * a.q_stride +
+                     (kh * G + (r0 + r - tq * G)) * kKvDim + 32 * t;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) load8(q + 8 * i, *reinterpret_cast<float(*)[8]>(v + 8 * i));
-    } else {
+        for (int i = 0; i < 4; ++i) load8(q + 8 * i, *reinterpret_cast<float(*)[8]>(v + 8 * i));
+      } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    }
-    float m = 0.f;
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      }
+      float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int e = max(-110, min(120, (int)(__float_as_uint(m) >> 23) - 127 - 7));  // m * 2^-e in [2^7, 2^8)
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    const float c = a.coef * __uint_as_float((uint32_t)(127 + e) << 23);
-    coef[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-    coef[nt][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = max(-110, min(120, (int)(__float_as_uint(m) >> 23) - 127 - 7));  // m * 2^-e in [2^7, 2^8)
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      const float c = a.coef * __uint_as_float((uint32_t)(127 + e) << 23);
+      coef[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+      coef[nt][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t hi[2], lo[2];
+      for (int j = 0; j < 8; ++j) {
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x = v[4 * j + 2 * i] * down, y = v[4 * j + 2 * i + 1] * down;
+          hi[i] = pack_f16(x, y);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+          lo[i] = pack_f16(x - f.x, y - f.y);
+        }
+        if constexpr (kQReg) {
+          qf[0][j][0] = hi[0];
+          qf[0][j][1] = hi[1];
+          if constexpr (P == 2) {
+            qf[1][j][0] = lo[0];
+            qf[1][j][1] = lo[1];
+          }
+        } else if (warp == nt % kWarps) {
+          sq[((nt * P) * 8 + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
+          if constexpr (P == 2) sq[((nt * P + 1) * 8 + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float x = v[4 * j + 2 * i] * down, y = v[4 * j + 2 * i + 1] * down;
-        hi[i] = pack_f16(x, y);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-        lo[i] = pack_f16(x - f.x, y - f.y);
+        const int rr = min(nt * 8 + 2 * t + i, rows - 1), tq = (r0 + rr) / G;
+        pq[nt][i] = len - a.Tq + tq;
+        slope[nt][i] = a.slopes ? __ldg(a.slopes + kh * G + (r0 + rr - tq * G)) * kLog2e : 0.f;
       }
-      if constexpr (kQReg) {
-        qf[0][j][0] = hi[0];
-        qf[0][j][1] = hi[1];
-        if constexpr (P == 2) {
-          qf[1][j][0] = lo[0];
-          qf[1][j][1] = lo[1];
+    }
+    if constexpr (!kQReg) named_barrier<32 * kWarps>();
+
+    float o[NT][8][4], M[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
+      M[nt][0] = M[nt][1] = kNoMax;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    // One tile.  FAST: every row sees all its tokens, and the scales are within f16's range (fast_scales).
+    const auto tile = [&](auto fast_c, const St& st, int j0, uint32_t there) {
+      constexpr bool FAST = decltype(fast_c)::value;
+      const int at = warp * kTok;  // the tile in the stage
+      const uint8_t* kc = st.k + at * kKvCodeBytes + tk * kKvCodeBytes + 16 * t;
+      const uint8_t* vc = st.v + at * kKvCodeBytes + t * kKvCodeBytes + 8 * g;
+      const uint32_t* ksp = st.ks + at + tk;
+      const uint32_t* vsp = st.vs + at + t;
+      // position of token k of the tile, -1 where none is
+      const auto pos_at = [&](int k) { return LIST ? st.pos[at + k] : (there >> (k >> 4)) & 1u ? j0 + k : -1; };
+      // ---- scores: S[token][row] = K q^T
+      float s[H][NT][4];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[h][nt][c] = 0.f;
+        uint32_t f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w = ksp[16 * h + 8 * i];
+          if constexpr (FAST) f[i] = fast_factor(__byte_perm(w, 0, 0x4040 + 0x0101 * t));
+          else f[i] = group_factor(w, t, top_scale(w)) * 0x10001u;
         }
-      } else if (warp == 0) {
-        sq[((nt * P) * 8 + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
-        if constexpr (P == 2) sq[((nt * P + 1) * 8 + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
-      }
-    }
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kc + 16 * h * kKvCodeBytes);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(kc + (16 * h + 8) * kKvCodeBytes);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = min(nt * 8 + 2 * t + i, rows - 1), tq = (r0 + rr) / G;
-      pq[nt][i] = len - a.Tq + tq;
-      slope[nt][i] = a.slopes ? __ldg(a.slopes + kh * G + (r0 + rr - tq * G)) * kLog2e : 0.f;
-    }
-  }
-  if constexpr (!kQReg) __syncthreads();
-
-  float o[NT][8][4], M[NT][2], l[NT][2];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t x[4], y[4];
+          e2m1x8_to_f16(w0[i], x);
+          e2m1x8_to_f16(w1[i], y);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t A[4] = {hmul2(x[2 * k], f[0]), hmul2(y[2 * k], f[1]), hmul2(x[2 * k + 1], f[0]),
+                                   hmul2(y[2 * k + 1], f[1])};
+            const int j = 2 * i + k;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
-    M[nt][0] = M[nt][1] = kNoMax;
-    l[nt][0] = l[nt][1] = 0.f;
-  }
-
-  const int32_t* table = a.c.table + b * a.c.table_stride;
-  const int64_t head_off = kh * a.c.head_stride;
-  const int scales_at = a.c.page_size * kKvCodeBytes;
-  const int tk = (g >> 1) + 4 * (g & 1);  // the token of key row g (row g + 8: + 8)
-
-  // ---- addresses.  Contiguous: the pages of the two 16-token halves of the
-  // next tile (-1: not there).  List: this lane's token.
-  int page[2] = {-1, -1}, pos_next = -1;
-  const auto find = [&](int n) {  // the pages (the token) of the tile at n
-    if constexpr (LIST) {
-      const int i = n + lane;
-      pos_next = i < n1 ? __ldg(a.idx + (int64_t)b * a.max_sel + i) : -1;
-      if (pos_next < 0 || pos_next >= len) pos_next = -1;
-      page[0] = pos_next >= 0 ? __ldg(table + page_index(a, pos_next)) : -1;
-      if (page[0] < 0 || page[0] >= a.c.n_pages) page[0] = pos_next = -1;
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        page[h] = n + 16 * h < n1 ? __ldg(table + page_index(a, n + 16 * h)) : -1;
-        if (page[h] >= a.c.n_pages) page[h] = -1;
-      }
-    }
-  };
-  uint4 kr[2][2];     // codes of tokens tk, tk + 8 of each half: dims 32t ..
-  uint2 vr[2][4];     // codes of tokens t + 4i of each half: dims 16g ..
-  uint32_t kw, vw;    // scales of token `lane`
-  int pos_cur;        // its position
-  int64_t row_off = 0;           // list: byte offset of this lane's token's codes (and its scales)
-  const uint8_t* base[2] = {};   // contiguous: offset of each half's codes in the pools
-  int64_t off[2] = {};
-  const auto load_k = [&](int n) {
-    if constexpr (LIST) {
-      const int pg = pos_next >= 0 ? page_index(a, pos_next) : 0;
-      const int slot = pos_next >= 0 ? pos_next - pg * a.c.page_size : 0;
-      const int64_t blk = max(page[0], 0) * a.c.page_stride + head_off;
-      row_off = blk + slot * kKvCodeBytes;
-      kw = __ldg(reinterpret_cast<const uint32_t*>(a.c.k + blk + scales_at + slot * kKvScaleBytes));
-      vw = __ldg(reinterpret_cast<const uint32_t*>(a.c.v + blk + scales_at + slot * kKvScaleBytes));
-      pos_cur = pos_next;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          kr[h][i] = ldg128(a.c.k + __shfl_sync(0xffffffffu, row_off, 16 * h + 8 * i + tk) + 16 * t);
-    } else {
-      int slot[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int pg = page_index(a, n + 16 * h);
-        slot[h] = page[h] >= 0 ? n + 16 * h - pg * a.c.page_size : 0;
-        off[h] = max(page[h], 0) * a.c.page_stride + head_off;
-      }
-      const int mine = lane >> 4;
-      const int64_t so = (mine ? off[1] : off[0]) + scales_at + ((mine ? slot[1] : slot[0]) + (lane & 15)) * kKvScaleBytes;
-      kw = __ldg(reinterpret_cast<const uint32_t*>(a.c.k + so));
-      vw = __ldg(reinterpret_cast<const uint32_t*>(a.c.v + so));
-      pos_cur = (mine ? page[1] : page[0]) >= 0 ? n + lane : -1;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        off[h] += slot[h] * kKvCodeBytes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) kr[h][i] = ldg128(a.c.k + off[h] + (8 * i + tk) * kKvCodeBytes + 16 * t);
-      }
-    }
-  };
-  const auto load_v = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (LIST) vr[h][i] = ldg64(a.c.v + __shfl_sync(0xffffffffu, row_off, 16 * h + 4 * i + t) + 8 * g);
-        else vr[h][i] = ldg64(a.c.v + off[h] + (4 * i + t) * kKvCodeBytes + 8 * g);
-      }
-  };
-
-  int n = n0 + warp * kTok;
-  if (n < n1) {
-    find(n);
-    load_k(n);
-    load_v();
-    find(n + kBlockTok);
-  }
-  for (; n < n1; n += kBlockTok) {
-    const bool v_nan = __any_sync(0xffffffffu, write_token(info + lane, kw, vw, pos_cur));
-    // every row sees every token of the tile
-    const bool whole = __all_sync(0xffffffffu, pos_cur >= lo_last && pos_cur <= p_first);
-    __syncwarp();
-    const bool more = n + kBlockTok < n1;
-    // ---- scores: S[token][row] = K q^T
-    float s[2][NT][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s[h][nt][c] = 0.f;
-      const uint32_t f0 = info[16 * h + tk].kf[t] * 0x10001u, f1 = info[16 * h + tk + 8].kf[t] * 0x10001u;
-      const uint32_t w0[4] = {kr[h][0].x, kr[h][0].y, kr[h][0].z, kr[h][0].w};
-      const uint32_t w1[4] = {kr[h][1].x, kr[h][1].y, kr[h][1].z, kr[h][1].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t x[4], y[4];
-        e2m1x8_to_f16(w0[i], x);
-        e2m1x8_to_f16(w1[i], y);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t A[4] = {hmul2(x[2 * k], f0), hmul2(y[2 * k], f1), hmul2(x[2 * k + 1], f0),
-                                 hmul2(y[2 * k + 1], f1)};
-          const int j = 2 * i + k;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-              if constexpr (kQReg) {
-                mma_f16(s[h][nt], A, qf[p][j][0], qf[p][j][1]);
-              } else {
-                const uint2 q2 = sq[((nt * P + p) * 8 + j) * 32 + lane];
-                mma_f16(s[h][nt], A, q2.x, q2.y);
+              for (int p = 0; p < P; ++p) {
+                if constexpr (kQReg) {
+                  mma_f16(s[h][nt], A, qf[p][j][0], qf[p][j][1]);
+                } else {
+                  const uint2 q2 = sq[((nt * P + p) * 8 + j) * 32 + lane];
+                  mma_f16(s[h][nt], A, q2.x, q2.y);
+                }
               }
-            }
+          }
         }
       }
-    }
-    if (more) {
-      // the next tile's keys; its values when this tile's are used up
-      // (off / row_off move on, so this tile's values must be here already)
-      load_k(n + kBlockTok);
-    }
-    // ---- softmax weights, in log2 units, times the value's size
-    uint32_t pf[2][NT][P][2];
-    {
-      float4 ti[2][2];
+      // ---- softmax weights in log2 units, times the value's size
+      float k_top[H][2], v_exp[H][2], v_inv[H][2];
+      if constexpr (!FAST) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ti[h][i] = *reinterpret_cast<const float4*>(info + 16 * h + 8 * i + tk);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = ksp[16 * h + 8 * i], r = top_scale(w);
+            k_top[h][i] = has_nan(w) ? nan_f32() : e8m0_value(r);
+            const uint32_t rv = top_value_scale(st.vs[at + 16 * h + 8 * i + tk]);
+            v_exp[h][i] = (float)((int)rv - 127);
+            v_inv[h][i] = rv < 254u ? __uint_as_float((254u - rv) << 23) : 0.5f * kMinNormal;
+          }
+      }
+      uint32_t pf[H][NT][P][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float u[2][4];  // [half][c]: rows tk, tk, tk + 8, tk + 8; columns 2t, 2t + 1, 2t, 2t + 1
+        float u[H][4];  // [half][c]: tokens tk, tk, tk + 8, tk + 8; columns 2t, 2t + 1, 2t, 2t + 1
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float4 w = ti[h][c >> 1];
-            float x = s[h][nt][c] * (coef[nt][c & 1] * w.x);
-            if (a.softcap > 0.f) {  // coef holds scale / softcap: cap * tanh(x) = cap - 2 cap / (1 + e^2x)
-              const float e2 = ex2(x * (2.f * kLog2e));
-              x = a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + e2);
-            }
-            const int j = __float_as_int(w.w);
-            if (a.slopes) x = fmaf(slope[nt][c & 1], (float)(j - pq[nt][c & 1]), x);
-            u[h][c] = x + w.y;
-          }
-        if (!whole) {
+          for (int c = 0; c < 4; ++c)
+            u[h][c] = s[h][nt][c] * (FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1]);
+        if (a.softcap > 0.f) {  // coef holds scale / softcap: cap * tanh(x) = cap - 2 cap / (1 + e^2x)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              u[h][c] = a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(u[h][c] * (2.f * kLog2e)));
+        }
+        if (a.slopes) {
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              u[h][c] = fmaf(slope[nt][c & 1], (float)(pos_at(16 * h + 8 * (c >> 1) + tk) - pq[nt][c & 1]), u[h][c]);
+        }
+        if constexpr (!FAST) {
+#pragma unroll
+          for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int j = __float_as_int(ti[h][c >> 1].w), p = pq[nt][c & 1];
-              if (j > p || j < low_of(p)) u[h][c] = -INFINITY;
+              const int j = pos_at(16 * h + 8 * (c >> 1) + tk), p = pq[nt][c & 1];
+              u[h][c] = j > p || j < low_of(p) ? -INFINITY : u[h][c] + v_exp[h][c >> 1];
             }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(fmaxf(u[0][i], u[0][i + 2]), fmaxf(u[1][i], u[1][i + 2]));
+          float m = fmaxf(u[0][i], u[0][i + 2]);
+          if constexpr (H == 2) m = fmaxf(m, fmaxf(u[1][i], u[1][i + 2]));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -441,12 +634,12 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const AttnArgs a) {
           }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
           float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             w[c] = ex2(u[h][c] - (M[nt][c & 1] - kLift));
-            l[nt][c & 1] = fmaf(w[c], ti[h][c >> 1].z, l[nt][c & 1]);
+            l[nt][c & 1] = FAST ? l[nt][c & 1] + w[c] : fmaf(w[c], v_inv[h][c >> 1], l[nt][c & 1]);
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -459,149 +652,274 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_kernel(const AttnArgs a) {
           }
         }
       }
-    }
-    if (v_nan) {  // a NaN scale makes its dimensions NaN for the rows that see the token, and for no other
-      for (int k = 0; k < kTok; ++k) {
-        if (info[k].vf[g >> 1] != 0x7fffu) continue;
-        const int j = info[k].pos;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (j <= pq[nt][i] && j >= low_of(pq[nt][i]))
-#pragma unroll
-              for (int d = 0; d < 8; ++d) o[nt][d][i] = o[nt][d][i + 2] = nan_f32();
-      }
-    }
-    // ---- outputs: O[dim][row] += V^T P^T
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t f[2];  // factors of tokens (t, t + 4) and (t + 8, t + 12) for dims 16g ..
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        f[i] = info[16 * h + 8 * i + t].vf[g >> 1] | ((uint32_t)info[16 * h + 8 * i + 4 + t].vf[g >> 1] << 16);
-      if (v_nan) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) f[i] &= ~__vcmpeq2(f[i], 0x7fff7fffu);
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // dims 16g .. +7, then +8 .. +15
-        uint32_t ev[2][4], od[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t wa = half ? vr[h][2 * i].y : vr[h][2 * i].x;
-          const uint32_t wb = half ? vr[h][2 * i + 1].y : vr[h][2 * i + 1].x;
-          e2m1x8_to_f16((wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u), ev[i]);
-          e2m1x8_to_f16(((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u), od[i]);
-        }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint32_t A[4] = {hmul2(ev[0][m], f[0]), hmul2(od[0][m], f[0]), hmul2(ev[1][m], f[1]),
-                                 hmul2(od[1][m], f[1])};
+      if constexpr (!FAST) {
+        // a NaN scale makes its dimensions NaN for the rows that see the token, and for no other
+#pragma unroll 1
+        for (int k = 0; k < kTok; ++k) {
+          if (byte_of(st.vs[at + k], grp) != 255u) continue;
+          const int j = pos_at(k);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int p = 0; p < P; ++p) mma_f16(o[nt][4 * half + m], A, pf[h][nt][p][0], pf[h][nt][p][1]);
+            for (int i = 0; i < 2; ++i)
+              if (j <= pq[nt][i] && j >= low_of(pq[nt][i]))
+#pragma unroll
+                for (int d = 0; d < 8; ++d) o[nt][d][i] = o[nt][d][i + 2] = nan_f32();
         }
       }
+      // ---- outputs: O[dim][row] += V^T P^T
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        uint32_t f[2];  // factors of tokens (t, t + 4) and (t + 8, t + 12) for dims 16g ..
+        uint2 vr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[i] = *reinterpret_cast<const uint2*>(vc + (16 * h + 4 * i) * kKvCodeBytes);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t wa = vsp[16 * h + 8 * i], wb = vsp[16 * h + 8 * i + 4];
+          if constexpr (FAST) {
+            f[i] = fast_factor(__byte_perm(wa, wb, 0x4400 + 0x1111 * grp) & 0x00ff00ffu);
+          } else {
+            const uint32_t fa = byte_of(wa, grp) == 255u ? 0u : group_factor(wa, grp, top_value_scale(wa));
+            const uint32_t fb = byte_of(wb, grp) == 255u ? 0u : group_factor(wb, grp, top_value_scale(wb));
+            f[i] = fa | (fb << 16);
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // dims 16g .. +7, then +8 .. +15
+          uint32_t ev[2][4], od[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t wa = half ? vr[2 * i].y : vr[2 * i].x, wb = half ? vr[2 * i + 1].y : vr[2 * i + 1].x;
+            e2m1x8_to_f16((wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u), ev[i]);
+            e2m1x8_to_f16(((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u), od[i]);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t A[4] = {hmul2(ev[0][m], f[0]), hmul2(od[0][m], f[0]), hmul2(ev[1][m], f[1]),
+                                   hmul2(od[1][m], f[1])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int p = 0; p < P; ++p) mma_f16(o[nt][4 * half + m], A, pf[h][nt][p][0], pf[h][nt][p][1]);
+          }
+        }
+      }
+    };
+    for (int i = wk.i0; i < wk.i1; ++i) {
+      const St& st = stages[stage];
+      const int j0 = rg.from + i * kBlock + warp * kTok;  // the tile's first token (list: entry)
+      // a wait that ran out ends the work, not the walk: the barriers below want every warp
+      if (ok) ok = mbar_wait_bounded(&full[stage], phase, &abort_flag, &g_kv4_err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        const uint32_t kw = st.ks[warp * kTok + (lane & (kTok - 1))], vw = st.vs[warp * kTok + (lane & (kTok - 1))];
+        const uint32_t there = LIST ? 0u : (st.there >> (warp * H)) & ((1u << H) - 1u);
+        bool mine = fast_scales(kw) && fast_scales(vw);
+        bool any;  // some row may see something
+        if constexpr (LIST) {
+          const int j = st.pos[warp * kTok + (lane & (kTok - 1))];
+          mine = mine && j >= lo_last && j <= p_first;
+          any = j0 < rg.to;
+        } else {
+          mine = mine && j0 >= lo_last && j0 + kTok - 1 <= p_first && there == (1u << H) - 1u;
+          any = j0 <= p_last && there != 0u;
+        }
+        if (__all_sync(0xffffffffu, mine)) tile(std::true_type{}, st, j0, there);
+        else if (any) tile(std::false_type{}, st, j0, there);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+      }
+      advance();
     }
-    __syncwarp();  // the infos are read
-    if (more) {
-      load_v();
-      find(n + 2 * kBlockTok);
-    }
-  }
 
-  // ---- the four warps' sums merged in shared memory
+    // ---- the warps' sums merged in shared memory: those from 4 on add to the first ones, then those from 2 on, then the second
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);                       // [warp][row][kORow]
-  float2* sml = reinterpret_cast<float2*>(so + kWarps * kRows * kORow);  // [warp][row]
+        for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
+#pragma unroll 1
+    for (int half = 4; half > 0; half >>= 1) {
+      if (warp >= half && warp < 2 * half) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* row = so + (warp * kRows + nt * 8 + 2 * t + i) * kORow;
+          for (int i = 0; i < 2; ++i) {
+            const int r = nt * 8 + 2 * t + i;
+            float* row = so + ((warp - half) * kRows + r) * kORow;
 #pragma unroll
-      for (int d = 0; d < 8; ++d)  // dims 16g + 2d, + 1 at 16d + 2g, + 1
-        *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[nt][d][i], o[nt][d][i + 2]);
-      if (g == 0) sml[warp * kRows + nt * 8 + 2 * t + i] = make_float2(M[nt][i], l[nt][i]);
+            for (int d = 0; d < 8; ++d)  // dims 16g + 2d, + 1 at 16d + 2g, + 1
+              *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[nt][d][i], o[nt][d][i + 2]);
+            if (g == 0) sml[warp - half][r] = make_float2(M[nt][i], l[nt][i]);
+          }
+      }
+      named_barrier<32 * kWarps>();
+      if (warp < half && warp + half < kWarps) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = nt * 8 + 2 * t + i;
+            const float* row = so + (warp * kRows + r) * kORow;
+            const float2 ml = sml[warp][r];
+            const float m = fmaxf(M[nt][i], ml.x), f0 = ex2(M[nt][i] - m), f1 = ex2(ml.x - m);
+            M[nt][i] = m;
+            l[nt][i] = l[nt][i] * f0 + ml.y * f1;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              const float2 x = *reinterpret_cast<const float2*>(row + 16 * d + 2 * g);
+              o[nt][d][i] = o[nt][d][i] * f0 + x.x * f1;
+              o[nt][d][i + 2] = o[nt][d][i + 2] * f0 + x.y * f1;
+            }
+          }
+      }
+      named_barrier<32 * kWarps>();
     }
-  }
-  __syncthreads();
-  const int d = threadIdx.x;
-  const int at = ((d & 15) >> 1) * 16 + (d >> 4) * 2 + (d & 1);
-  for (int r = 0; r < rows; ++r) {
-    float m = kNoMax, num = 0.f, den = 0.f;
+    // the first warp has the sums; all of them write them out
+    if (warp == 0) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * kRows + r].x);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sml[w * kRows + r];
-      const float f = ex2(ml.x - m);
-      den = fmaf(f, ml.y, den);
-      num = fmaf(f, so[(w * kRows + r) * kORow + at], num);
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
+          float* row = so + r * kORow;
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[nt][d][i], o[nt][d][i + 2]);
+          if (g == 0) sml[0][r] = make_float2(M[nt][i], l[nt][i]);
+        }
     }
-    const int64_t R = part_row(r);
-    if (a.splits > 1) {
-      a.part_o[(R * a.splits + split) * kKvDim + d] = num;
-      if (d == 0) a.part_ml[R * a.splits + split] = make_float2(den == 0.f ? -INFINITY : m, den);
-    } else {
-      store1(static_cast<T*>(a.out) + R * kKvDim + d, den == 0.f ? 0.f : num / den);
+    named_barrier<32 * kWarps>();
+    for (int x = threadIdx.x; x < rows * kKvDim; x += 32 * kWarps) {
+      const int r = x / kKvDim, d = x % kKvDim;
+      const float num = so[r * kORow + ((d & 15) >> 1) * 16 + (d >> 4) * 2 + (d & 1)], den = sml[0][r].y;
+      if (complete) {
+        store1(static_cast<T*>(a.out) + out_row(a, wk.b, kh, G, r0 + r) * kKvDim + d, den == 0.f ? 0.f : num / den);
+      } else {
+        const int64_t R = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
+        a.part_o[R * kKvDim + d] = num;
+        if (d == 0) a.part_ml[R] = sml[0][r];
+      }
     }
+    slot = 1;
+    named_barrier<32 * kWarps>();  // the shared memory is used again
   }
 }
 
-// out[row] = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s: one CTA a row, a
-// dimension a thread.
-template <class T>
-__global__ void __launch_bounds__(kKvDim) kv4_combine_kernel(const float* __restrict__ part_o,
-                                                             const float2* __restrict__ part_ml, int splits,
-                                                             T* __restrict__ out) {
+// Merges the parts of the units that several CTAs share.  CTA c looks at what
+// CTA c + 1 of the attention said of the unit in which its range begins; out =
+// sum 2^(m_s - m) o_s / sum 2^(m_s - m) l_s, a lane four dimensions.  WIDE (few
+// units, many parts): a CTA a row, the parts shared by its eight warps;
+// otherwise a warp a row.
+constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32;
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const AttnArgs a, int tile_rows) {
+  __shared__ float4 so[WIDE ? kCombineThreads : 1];
+  __shared__ float2 sml[kCombineWarps];
   grid_dependency_wait();
-  const int64_t R = blockIdx.x;
-  const int d = threadIdx.x;
-  const float2* ml = part_ml + R * splits;
-  float m = -INFINITY;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, __ldg(ml + s).x);
-  float num = 0.f, den = 0.f;
-  if (m != -INFINITY)
-    for (int s = 0; s < splits; ++s) {
-      const float2 x = __ldg(ml + s);
-      if (x.x == -INFINITY) continue;  // nothing there: no output was written
-      const float f = ex2(x.x - m);
-      den = fmaf(f, x.y, den);
-      num = fmaf(f, __ldg(part_o + (R * splits + s) * kKvDim + d), num);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int4 raw = __ldcg(reinterpret_cast<const int4*>(a.share + blockIdx.x + 1));
+  const Share sh = {raw.x, raw.y, raw.z, raw.w};
+  if (sh.b < 0) return;
+  const int G = a.n_q / a.c.n_heads, kh = sh.unit / a.row_tiles, r0 = (sh.unit - kh * a.row_tiles) * tile_rows;
+  const int rows = min(tile_rows, a.Tq * G - r0);
+  constexpr int kStep = WIDE ? kCombineWarps : 1, kUnroll = 8;
+  for (int r = WIDE ? blockIdx.y : warp; r < rows; r += WIDE ? gridDim.y : kCombineWarps) {
+    float m = kNoMax, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = WIDE ? warp : 0; i0 < sh.parts; i0 += kUnroll * kStep) {
+      float2 ml[kUnroll];
+      float4 o[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int i = i0 + k * kStep;
+        ml[k] = make_float2(kNoMax, 0.f);
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < sh.parts) {
+          const int64_t at = (int64_t)(i == 0 ? sh.slot0 : 2 * ((int)blockIdx.x + i)) * tile_rows + r;
+          ml[k] = __ldcg(a.part_ml + at);
+          o[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kKvDim) + lane);
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) mn = fmaxf(mn, ml[k].x);
+      const float f0 = ex2(m - mn);
+      m = mn;
+      den *= f0;
+      num = make_float4(num.x * f0, num.y * f0, num.z * f0, num.w * f0);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const float f = ex2(ml[k].x - m);
+        den = fmaf(f, ml[k].y, den);
+        num = make_float4(fmaf(f, o[k].x, num.x), fmaf(f, o[k].y, num.y), fmaf(f, o[k].z, num.z), fmaf(f, o[k].w, num.w));
+      }
     }
-  store1(out + R * kKvDim + d, den == 0.f ? 0.f : num / den);
+    if constexpr (WIDE) {
+      so[threadIdx.x] = num;
+      if (lane == 0) sml[warp] = make_float2(m, den);
+      __syncthreads();
+      if (warp == 0) {
+        m = kNoMax;
+#pragma unroll
+        for (int i = 0; i < kCombineWarps; ++i) m = fmaxf(m, sml[i].x);
+        den = 0.f;
+        num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kCombineWarps; ++i) {
+          const float f = ex2(sml[i].x - m);
+          const float4 v = so[32 * i + lane];
+          den = fmaf(f, sml[i].y, den);
+          num = make_float4(fmaf(f, v.x, num.x), fmaf(f, v.y, num.y), fmaf(f, v.z, num.z), fmaf(f, v.w, num.w));
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    T* out = static_cast<T*>(a.out) + out_row(a, sh.b, kh, G, r0 + r) * kKvDim + 4 * lane;
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    store1(out, num.x * inv);
+    store1(out + 1, num.y * inv);
+    store1(out + 2, num.z * inv);
+    store1(out + 3, num.w * inv);
+  }
 }
 
-// How a call is cut: row tiles of 8 * nt query rows, and splits of `chunk` tokens.
+// How a call is cut: units (a row's kv head and a tile of 8 * nt query rows)
+// times blocks of tokens, shared evenly by as many CTAs as the GPU holds at once,
+// however the rows' lengths differ.
 struct AttnPlan {
-  int nt, row_tiles, chunk, splits;
+  int nt, row_tiles, block, grid;
+  bool wide;  // few units: each is shared by many CTAs
 };
 
 constexpr int kSms = 148;
 
 AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   AttnPlan p;
-  const int rows = d->Tq * (d->n_q_heads / c->n_kv_heads);
+  const int rows = d->Tq * (d->n_q_heads / c->n_kv_heads), pieces = d->dtype == FM_F32 ? 2 : 1;
   p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   p.row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
   int64_t tokens = d->idx ? d->max_sel : d->max_len;
-  if (!d->idx && d->window > 0)  // a row tile reaches back window + Tq - 1 from the last token, from a multiple of 32
-    tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kTok - 1);
+  if (!d->idx && d->window > 0)  // a row reaches back window + Tq - 1 from the last token, from a multiple of 32
+    tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kMaxRunTok - 1);
   const int64_t units = (int64_t)c->B * c->n_kv_heads * p.row_tiles;
-  const int64_t want = (tokens * units + 12 * kSms - 1) / (12 * kSms);
-  const int64_t chunk = std::max<int64_t>(kBlockTok, std::min<int64_t>((want + kBlockTok - 1) / kBlockTok * kBlockTok, 4096));
-  p.chunk = (int)chunk;
-  p.splits = (int)((tokens + chunk - 1) / chunk);
+  p.block = block_tokens(p.nt, pieces);
+  p.grid = (int)std::min<int64_t>(units * ((tokens + p.block - 1) / p.block), kSms * ctas_per_sm(p.nt));
+  p.wide = 8 * units <= p.grid;
   return p;
+}
+
+// Bytes of the workspace's parts.
+struct AttnSpace {
+  size_t share, ml, o;
+  size_t total() const { return share + ml + o; }
+};
+AttnSpace space_of(const AttnPlan& p) {
+  const size_t rows = (size_t)p.grid * 2 * 8 * p.nt;
+  return {((size_t)p.grid * sizeof(Share) + 15) / 16 * 16, rows * sizeof(float2), rows * kKvDim * sizeof(float)};
 }
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -620,35 +938,49 @@ fm_status check_attn(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
 }
 
 }  // namespace
+
+int take_kv4_error() {
+  int h = kDevErrNone;
+  if (cudaMemcpyFromSymbol(&h, g_kv4_err, sizeof(int)) != cudaSuccess) {
+    cudaGetLastError();
+    return kDevErrNone;
+  }
+  if (h != kDevErrNone) {
+    const int zero = kDevErrNone;
+    cudaMemcpyToSymbol(g_kv4_err, &zero, sizeof(int));
+  }
+  return h;
+}
+
 }  // namespace fm
 
 using namespace fm;
 
 extern "C" size_t fm_kv4_attention_workspace_bytes(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   if (check_attn(c, d) != FM_OK) return 0;
-  const AttnPlan p = plan_of(c, d);
-  if (p.splits == 1) return 16;
-  return (size_t)c->B * d->Tq * d->n_q_heads * p.splits * (kKvDim + 2) * sizeof(float);
+  return space_of(plan_of(c, d)).total();
 }
 
 namespace {
 
 template <class T, int NT, int P, bool LIST>
-fm_status launch_attn(const AttnArgs& a, dim3 grid, cudaStream_t stream) {
-  constexpr int kLoop = kWarps * kTok * (int)sizeof(TokenInfo) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2));
-  constexpr int kEnd = kWarps * 8 * NT * (kORow * (int)sizeof(float) + (int)sizeof(float2));
-  constexpr int kSmem = kLoop > kEnd ? kLoop : kEnd;
+fm_status launch_attn(const AttnArgs& a, int grid, cudaStream_t stream) {
+  using S = Shape<NT, P>;
+  static_assert(S::kBlock == block_tokens(NT, P) && S::kCtas == ctas_per_sm(NT), "the host's plan is the kernel's");
+  constexpr int kSmem = S::kStages * (int)sizeof(Stage<S::kBlock>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
+                        S::kMergers * S::kRows * kORow * (int)sizeof(float);
+  static_assert(kSmem * S::kCtas <= 225 * 1024, "shared memory of an SM");
   static PerDeviceOnce once;
   int dev = 0;
   cudaGetDevice(&dev);
   if (fm_status s = smem_limit_once(once, dev, kv4_attn_kernel<T, NT, P, LIST>, kSmem)) return s;
-  kv4_attn_kernel<T, NT, P, LIST><<<grid, kThreads, kSmem, stream>>>(a);
+  kv4_attn_kernel<T, NT, P, LIST><<<grid, S::kThreads, kSmem, stream>>>(a);
   note_launch();
   return check_launch();
 }
 
 template <class T, bool LIST>
-fm_status launch_attn_nt(const AttnArgs& a, int nt, dim3 grid, cudaStream_t stream) {
+fm_status launch_attn_nt(const AttnArgs& a, int nt, int grid, cudaStream_t stream) {
   constexpr int P = sizeof(T) == 4 ? 2 : 1;
   if (nt == 1) return launch_attn<T, 1, P, LIST>(a, grid, stream);
   if (nt == 2) return launch_attn<T, 2, P, LIST>(a, grid, stream);
@@ -668,8 +1000,7 @@ extern "C" fm_status fm_kv4_attention(const fm_kv4_cache* c, const fm_kv4_attn_d
     return FM_ERR_ALIGNMENT;
   if (ws_bytes < fm_kv4_attention_workspace_bytes(c, d)) return FM_ERR_INVALID_ARG;
   const AttnPlan p = plan_of(c, d);
-  const int64_t rows = (int64_t)c->B * d->Tq * d->n_q_heads;
-  if ((int64_t)c->n_kv_heads * p.row_tiles > 65535) return FM_ERR_UNSUPPORTED;
+  const AttnSpace sp = space_of(p);
   AttnArgs a = {};
   a.c = kv4_view(*c);
   a.q = d->q;
@@ -691,19 +1022,21 @@ extern "C" fm_status fm_kv4_attention(const fm_kv4_cache* c, const fm_kv4_attn_d
   const int q16 = c->page_size / 16;
   a.page_magic = q16 == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q16 - 1) / q16);
   a.row_tiles = p.row_tiles;
-  a.chunk = p.chunk;
-  a.splits = p.splits;
-  a.part_o = static_cast<float*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (p.splits > 1 ? rows * p.splits * kKvDim : 0));
-  const dim3 grid(p.splits, c->n_kv_heads * p.row_tiles, c->B);
+  a.run = std::min(c->page_size & -c->page_size, p.nt == 4 ? 16 : kMaxRunTok);
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  a.share = reinterpret_cast<Share*>(at);
+  a.part_ml = reinterpret_cast<float2*>(at + sp.share);
+  a.part_o = reinterpret_cast<float*>(at + sp.share + sp.ml);
   return by_dtype(d->dtype, [&](auto* tag) -> fm_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    const fm_status s = d->idx ? launch_attn_nt<T, true>(a, p.nt, grid, stream)
-                               : launch_attn_nt<T, false>(a, p.nt, grid, stream);
-    if (s != FM_OK || p.splits == 1) return s;
-    const cudaError_t e = launch_overlapped(kv4_combine_kernel<T>, dim3((unsigned)rows), dim3(kKvDim), 0, stream,
-                                            (const float*)a.part_o, (const float2*)a.part_ml, p.splits,
-                                            static_cast<T*>(d->out));
+    const fm_status s = d->idx ? launch_attn_nt<T, true>(a, p.nt, p.grid, stream)
+                               : launch_attn_nt<T, false>(a, p.nt, p.grid, stream);
+    if (s != FM_OK || p.grid == 1) return s;
+    const cudaError_t e =
+        p.wide ? launch_overlapped(kv4_combine_kernel<T, true>, dim3(p.grid - 1, 8 * p.nt), dim3(kCombineThreads), 0,
+                                   stream, a, 8 * p.nt)
+               : launch_overlapped(kv4_combine_kernel<T, false>, dim3(p.grid - 1), dim3(kCombineThreads), 0, stream, a,
+                                   8 * p.nt);
     if (e != cudaSuccess) return record_cuda_error(e);
     note_launch();
     return check_launch();
