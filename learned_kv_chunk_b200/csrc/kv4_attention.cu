@@ -25,7 +25,7 @@ struct AttnArgs {
   float coef, softcap, cap_log2;
   uint32_t page_magic;  // ceil(2^32 / (page_size / 16)), 0 for a page of 16
   int row_tiles;
-  int run;              // tokens that lie together wherever they are: the largest power of two in a page
+  int run;              // tokens that lie together: the largest power of two in a page, at most a block; list: a block
   // the partial results of units that several CTAs share: two slots a CTA, its first segment's and its last's
   struct Share* share;  // [CTAs]
   float2* part_ml;      // [CTAs][2][rows of a tile]: the maximum (log2 units), the sum
@@ -41,24 +41,22 @@ struct Share {
 
 // A CTA has consumer warps and a producer warp, together a multiple of what fills
 // the four schedulers' register files: 16 warps of 128 registers an SM where 8
-// rows suffice, 12 of 168 for 16 rows or two pieces, 8 of 255 for 32 rows.  A
-// stage holds a block of tokens: a tile (16 tokens, or twice 16) for each
-// consumer.
-constexpr int kMaxRunTok = 32;
+// rows and one piece suffice, 12 of 168 for 16 rows or two pieces.  More query
+// rows of a kv head make more units (tiles of 32 rows, at 255 registers and 8
+// warps an SM, took 1.4 times as long as two of 16 on 32-row calls).  A stage
+// holds a block of four tiles of 32 tokens; the consumers take a segment's tiles
+// as they come free.
+constexpr int kTok = 32;
+constexpr int kBlock = 128;  // tokens of a stage, the unit in which work is shared out
+constexpr int kTiles = kBlock / kTok;
 template <int NT, int P>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kHalves = NT == 4 ? 1 : 2;      // 16-token halves of a tile: 32 rows leave registers for one
-  static constexpr int kTok = 16 * kHalves;
-  static constexpr int kWarps = NT == 4 || (NT == 1 && P == 1) ? 7 : 5;  // consumers
-  static constexpr int kBlock = kWarps * kTok;         // tokens of a stage, the unit in which work is shared out
-  static constexpr int kCtas = NT == 4 ? 1 : 2;        // that an SM holds
-  static constexpr int kStages = NT == 4 ? 6 : 3;
+  static constexpr int kWarps = NT == 1 && P == 1 ? 7 : 5;  // consumers
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kMergers = 3;                   // the most warps that add to others at once
 };
-constexpr int block_tokens(int nt, int pieces) { return nt == 4 ? 112 : nt == 1 && pieces == 1 ? 224 : 160; }
-constexpr int ctas_per_sm(int nt) { return nt == 4 ? 1 : 2; }
+constexpr int kCtas = 2;     // that an SM holds
+constexpr int stages(int nt, bool list) { return nt == 1 ? (list ? 5 : 6) : 4; }
 
 constexpr float kNoMax = -1e30f;          // the running maximum of a row that has seen nothing
 constexpr float kLazy = 6.f;              // the maximum may be exceeded by 2^6 before the sums are rescaled
@@ -70,6 +68,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // The four code bytes of w as four f16 pairs (low nibble in the low half).
@@ -127,10 +133,12 @@ __device__ int g_kv4_err;  // kDevErrTimeout once a wait of the attention's ran 
 // products with a code are exact.  Any other tile takes the general form: each
 // record's factors are relative to its largest scale 2^r, which multiplies the
 // score (keys) or joins the weight's exponent (values).
-__device__ __forceinline__ bool fast_scales(uint32_t w) {
+__device__ __forceinline__ bool fast_scales(uint32_t a, uint32_t b) {
   // bytes + 116 in [224, 255] is [108, 139], + 15 in [128, 255] is [113, 240]; a
   // byte that carries into its neighbour fails the first test itself
-  return (((w + 0x74747474u) & 0xe0e0e0e0u) == 0xe0e0e0e0u) && (((w + 0x0f0f0f0fu) & 0x80808080u) == 0x80808080u);
+  const uint32_t t = ((a + 0x74747474u) & (b + 0x74747474u)) | 0x1f1f1f1fu;
+  const uint32_t s = ((a + 0x0f0f0f0fu) & (b + 0x0f0f0f0fu)) | 0x7f7f7f7fu;
+  return (t & s) == 0xffffffffu;
 }
 // Two f16 factors from the bytes 0 and 2 of p (bytes 1 and 3 are 0).
 __device__ __forceinline__ uint32_t fast_factor(uint32_t p) { return p * 1024u - 112u * 1024u * 65537u; }
@@ -157,13 +165,14 @@ __device__ __forceinline__ uint32_t group_factor(uint32_t w, int i, uint32_t r) 
   return __half_as_ushort(h);
 }
 
-// A block in shared memory.
-template <int BLOCK>
-struct alignas(128) Stage {
-  uint8_t k[BLOCK * kKvCodeBytes], v[BLOCK * kKvCodeBytes];
-  uint32_t ks[BLOCK], vs[BLOCK];
-  int pos[BLOCK];   // list: the entries' positions, -1: none
-  uint32_t there;   // no list: bit i, tokens 16i .. 16i + 15 are there
+// A block in shared memory: of the keys and of the values, runs of `run` tokens,
+// each the codes of its tokens and then their scales, as a page's block has them
+// (a page of at most 128 tokens, a power of two, is one run and one copy).
+template <bool LIST>
+struct alignas(16) Stage {
+  uint8_t k[kBlock * kKvBytes], v[kBlock * kKvBytes];
+  int pos[LIST ? kBlock : 1];  // the entries' positions, -1: none
+  uint32_t there;              // no list: bit i, tokens 16i .. 16i + 15 are there
 };
 
 constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
@@ -176,11 +185,13 @@ __device__ __forceinline__ int page_index(const AttnArgs& a, int pos) {
 
 // What a row holds: its length and first visible position, its tokens (list
 // entries) [from, to), cut into blocks; one block even if it has none, for its
-// output.
+// output.  A unit costs its blocks and kUnitCost more (its queries, the merge of
+// its warps' sums): work is shared out by that cost.
+constexpr int kUnitCost = 4;
 struct Range {
-  int len, start, from, to, blocks;
+  int len, start, from, to, blocks, cost;
 };
-template <int BLOCK, bool LIST>
+template <bool LIST>
 __device__ __forceinline__ Range row_range(const AttnArgs& a, int b) {
   Range r;
   r.len = max(0, min(__ldg(a.kv_len + b), a.max_len));
@@ -190,10 +201,11 @@ __device__ __forceinline__ Range row_range(const AttnArgs& a, int b) {
     r.to = max(0, min(__ldg(a.count + b), a.max_sel));
   } else {
     const int p = r.len - a.Tq;  // the first query's position
-    r.from = (a.window > 0 ? max(r.start, p - a.window + 1) : r.start) & ~(kMaxRunTok - 1);
+    r.from = (a.window > 0 ? max(r.start, p - a.window + 1) : r.start) & ~(kBlock - 1);
     r.to = r.len;
   }
-  r.blocks = max(1, (r.to - r.from + BLOCK - 1) / BLOCK);
+  r.blocks = max(1, (r.to - r.from + kBlock - 1) / kBlock);
+  r.cost = r.blocks + kUnitCost;
   return r;
 }
 
@@ -214,113 +226,156 @@ __device__ __forceinline__ void named_barrier() {
 
 // The walk over a CTA's blocks: segments of units (a row's kv head and tile of
 // query rows), in the same order for the producer and the consumers.
-template <int BLOCK, bool LIST>
+template <bool LIST>
 struct Walk {
-  int64_t w, end, base;  // next block, the range's end, blocks of the rows before b (for one unit)
+  int64_t w, end, base;  // where it is and ends among all costs; the cost of the rows before b (for one unit)
   int b, units;
   Range rg;
-  // the current segment
+  // the current segment: blocks [i0, i1) of a unit; i1 = i0 where only a unit's extra cost lies in the range
   int unit, i0, i1;
+  int64_t next_w;
   __device__ __forceinline__ void segment() {
     const int64_t x = w - base * units;
-    unit = (int)div_small(x, rg.blocks);
-    i0 = (int)(x - (int64_t)unit * rg.blocks);
-    i1 = (int)min((int64_t)rg.blocks, i0 + (end - w));
+    unit = (int)div_small(x, rg.cost);
+    const int x0 = (int)(x - (int64_t)unit * rg.cost), x1 = (int)min((int64_t)rg.cost, x0 + (end - w));
+    next_w = w + (x1 - x0);
+    i0 = min(x0, rg.blocks);
+    i1 = min(x1, rg.blocks);
   }
+  __device__ __forceinline__ bool more() const { return w < end; }
   __device__ __forceinline__ void next(const AttnArgs& a) {
-    w += i1 - i0;
-    if (w < end && w == (base + rg.blocks) * units) {  // the next row
-      base += rg.blocks;
-      rg = row_range<BLOCK, LIST>(a, ++b);
+    w = next_w;
+    if (w >= end) return;
+    if (w == (base + rg.cost) * units) {  // the next row
+      base += rg.cost;
+      rg = row_range<LIST>(a, ++b);
     }
+    segment();
   }
 };
 
 template <class T, int NT, int P, bool LIST>
-__global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) kv4_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel(const AttnArgs a) {
   using S = Shape<NT, P>;
-  constexpr int kRows = S::kRows, H = S::kHalves, kTok = S::kTok, kBlock = S::kBlock, kWarps = S::kWarps;
-  constexpr int kStages = S::kStages;
+  constexpr int kRows = S::kRows, H = 2, kWarps = S::kWarps;  // H: 16-token halves of a tile
   constexpr bool kQReg = NT == 1;
-  using St = Stage<kBlock>;
+  using St = Stage<LIST>;
+  constexpr int kStages = stages(NT, LIST);
   extern __shared__ __align__(128) uint8_t smem[];
-  St* stages = reinterpret_cast<St*>(smem);
+  St* ring = reinterpret_cast<St*>(smem);
   // the queries, when they are not kept in registers, then the merge's outputs of half of the warps
-  uint2* sq = reinterpret_cast<uint2*>(stages + kStages);
+  uint2* sq = reinterpret_cast<uint2*>(ring + kStages);
   float* so = reinterpret_cast<float*>(sq + (kQReg ? 0 : NT * P * 8 * 32));
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int64_t sums[kWarps + 1], found[2];
-  __shared__ float2 sml[S::kMergers][kRows];
+  __shared__ float2 sml[2][kRows];
   __shared__ int abort_flag;
+  __shared__ int4 place[kTiles];  // of a tile in a stage: its halves' codes and scales
+  __shared__ uint32_t next_tile;  // of the segment, after one for each consumer
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.n_q / a.c.n_heads;
 
   // ---- this CTA's share of the work
-  Walk<kBlock, LIST> wk;
+  Walk<LIST> wk;
   wk.units = a.c.n_heads * a.row_tiles;
   {
     if (threadIdx.x == 0) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&full[i], LIST ? 64 : 1);
-        mbar_init(&empty[i], kWarps);
+        mbar_init(&empty[i], kTiles);
       }
       abort_flag = 0;
+      next_tile = kWarps;
+      for (int i = 0; i < kTiles; ++i) {
+        const int t0 = kTok * i, t1 = t0 + 16, s0 = t0 / a.run, s1 = t1 / a.run;
+        place[i] = make_int4(s0 * a.run * kKvBytes + (t0 - s0 * a.run) * kKvCodeBytes,
+                             s0 * a.run * kKvBytes + a.run * kKvCodeBytes + (t0 - s0 * a.run) * kKvScaleBytes,
+                             s1 * a.run * kKvBytes + (t1 - s1 * a.run) * kKvCodeBytes,
+                             s1 * a.run * kKvBytes + a.run * kKvCodeBytes + (t1 - s1 * a.run) * kKvScaleBytes);
+      }
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // rows in order, `per` a thread
-    const int per = (a.c.B + S::kThreads - 1) / S::kThreads, first = threadIdx.x * per;
-    int64_t mine = 0;
-    for (int i = first; i < min(first + per, a.c.B); ++i) mine += row_range<kBlock, LIST>(a, i).blocks;
-    int64_t upto = mine;
+    int64_t total;
+    bool mine_to_do = true;
+    const auto take_share = [&] {  // of `total`
+      const int64_t n_cta = min((int64_t)gridDim.x, total);
+      mine_to_do = blockIdx.x < n_cta;
+      if (!mine_to_do) return;
+      wk.w = div_small(total * blockIdx.x, n_cta);
+      wk.end = div_small(total * (blockIdx.x + 1), n_cta);
+    };
+    if (a.c.B <= 32) {  // every warp finds its place by itself, a lane a row
+      const Range r = row_range<LIST>(a, min(lane, a.c.B - 1));
+      int upto = lane < a.c.B ? r.cost : 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += x;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    int64_t total = 0;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      total = (int64_t)__shfl_sync(0xffffffffu, upto, 31) * wk.units;
+      take_share();
+      wk.b = min(__popc(__ballot_sync(0xffffffffu, (int64_t)upto * wk.units <= wk.w)), a.c.B - 1);
+      wk.base = __shfl_sync(0xffffffffu, upto - r.cost, wk.b);
+      wk.rg = {__shfl_sync(0xffffffffu, r.len, wk.b),  __shfl_sync(0xffffffffu, r.start, wk.b),
+               __shfl_sync(0xffffffffu, r.from, wk.b), __shfl_sync(0xffffffffu, r.to, wk.b),
+               __shfl_sync(0xffffffffu, r.blocks, wk.b), __shfl_sync(0xffffffffu, r.cost, wk.b)};
+    } else {  // rows in order, `per` a thread
+      const int per = (a.c.B + S::kThreads - 1) / S::kThreads, first = threadIdx.x * per;
+      int64_t mine = 0;
+      for (int i = first; i < min(first + per, a.c.B); ++i) mine += row_range<LIST>(a, i).cost;
+      int64_t upto = mine;
 #pragma unroll
-    for (int i = 0; i < kWarps + 1; ++i) {
-      if (i < warp) upto += sums[i];
-      total += sums[i];
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+      }
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps + 1; ++i) {
+        if (i < warp) upto += sums[i];
+        total += sums[i];
+      }
+      total *= wk.units;
+      take_share();
+      int64_t before = upto - mine;
+      if (mine_to_do && wk.w >= before * wk.units && wk.w < upto * wk.units) {
+        int i = first;
+        for (;; ++i) {
+          const int cost = row_range<LIST>(a, i).cost;
+          if (wk.w < (before + cost) * wk.units) break;
+          before += cost;
+        }
+        found[0] = i;
+        found[1] = before;
+      }
+      __syncthreads();
+      if (mine_to_do) {
+        wk.b = (int)found[0];
+        wk.base = found[1];
+        wk.rg = row_range<LIST>(a, wk.b);
+      }
     }
-    total *= wk.units;
-    const int64_t n_cta = min((int64_t)gridDim.x, total);
-    if (blockIdx.x >= n_cta) {
+    if (!mine_to_do) {
       if (threadIdx.x == 0) a.share[blockIdx.x].b = -1;
       return;
     }
-    wk.w = div_small(total * blockIdx.x, n_cta);
-    wk.end = div_small(total * (blockIdx.x + 1), n_cta);
-    int64_t before = upto - mine;
-    if (wk.w >= before * wk.units && wk.w < upto * wk.units) {
-      int i = first;
-      for (;; ++i) {
-        const int nb = row_range<kBlock, LIST>(a, i).blocks;
-        if (wk.w < (before + nb) * wk.units) break;
-        before += nb;
-      }
-      found[0] = i;
-      found[1] = before;
-    }
-    __syncthreads();
-    wk.b = (int)found[0];
-    wk.base = found[1];
-    wk.rg = row_range<kBlock, LIST>(a, wk.b);
     wk.segment();
-    if (threadIdx.x == 0) {
+    const int64_t n_cta = min((int64_t)gridDim.x, total);
+    if (threadIdx.x == 32) {
       // the CTAs c with total * c / n_cta <= x own block x: the last of them is ((x + 1) * n_cta - 1) / total
       Share sh = {-1, wk.unit, 0, 0};
-      const int64_t w0 = wk.w - wk.i0, w1 = w0 + wk.rg.blocks;
+      const int64_t w0 = wk.base * wk.units + (int64_t)wk.unit * wk.rg.cost, w1 = w0 + wk.rg.blocks;
       const int64_t prev = blockIdx.x ? (int64_t)div_small(total * (blockIdx.x - 1), n_cta) : 0;
-      if (wk.i0 > 0 && prev <= w0) {
+      if (wk.i0 > 0 && wk.i0 < wk.rg.blocks && prev <= w0) {
         sh.b = wk.b;
         sh.parts = (int)div_small(w1 * n_cta - 1, total) - (int)blockIdx.x + 2;
         sh.slot0 = 2 * ((int)blockIdx.x - 1) + (w0 > prev ? 1 : 0);
       }
       a.share[blockIdx.x] = sh;
     }
+    __syncthreads();  // the barriers are there
   }
 
   int stage = 0;
@@ -337,30 +392,40 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
     const int scales_at = a.c.page_size * kKvCodeBytes;
     bool ok = true;
     uint32_t filled = 0;  // stages whose copies are under way
-    for (; ok && wk.w < wk.end; wk.next(a), wk.segment()) {
+    for (; ok && wk.more(); wk.next(a)) {
       const int kh = wk.unit / a.row_tiles;
       const int32_t* table = a.c.table + wk.b * a.c.table_stride;
       const uint8_t* kp = a.c.k + kh * a.c.head_stride;
       const uint8_t* vp = a.c.v + kh * a.c.head_stride;
-      for (int i = wk.i0; i < wk.i1; ++i) {
+      // looked up a block ahead: list, the positions of entries lane + 32e; otherwise, a lane a run (`run` tokens of
+      // a page lie together), its page
+      constexpr int kPer = kBlock / 32;
+      int ahead[LIST ? kPer : 1];
+      const auto look = [&](int i) {
         const int n = wk.rg.from + i * kBlock;
-        St& st = stages[stage];
         if constexpr (LIST) {
-          constexpr int kPer = (kBlock + 31) / 32;
-          int pos[kPer], page[kPer], slot[kPer];  // of entries lane + 32e
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
             const int x = n + 32 * e + lane;
-            pos[e] = 32 * e + lane < kBlock && x < wk.rg.to ? __ldg(a.idx + (int64_t)wk.b * a.max_sel + x) : -1;
-            if (pos[e] < 0 || pos[e] >= wk.rg.len) pos[e] = -1;
+            ahead[e] = i < wk.i1 && x < wk.rg.to ? __ldg(a.idx + (int64_t)wk.b * a.max_sel + x) : -1;
           }
+        } else {
+          const int at = n + lane * a.run;
+          ahead[0] = i < wk.i1 && lane * a.run < kBlock && at < wk.rg.to ? __ldg(table + page_index(a, at)) : -1;
+        }
+      };
+      look(wk.i0);
+      for (int i = wk.i0; i < wk.i1; ++i) {
+        const int n = wk.rg.from + i * kBlock;
+        St& st = ring[stage];
+        if constexpr (LIST) {
+          int pos[kPer], page[kPer];
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
-            const int pg = pos[e] >= 0 ? page_index(a, pos[e]) : 0;
-            slot[e] = pos[e] - pg * a.c.page_size;
-            page[e] = pos[e] >= 0 ? __ldg(table + pg) : -1;
-            if (page[e] < 0 || page[e] >= a.c.n_pages) page[e] = pos[e] = -1;
+            pos[e] = ahead[e] < 0 || ahead[e] >= wk.rg.len ? -1 : ahead[e];
+            page[e] = pos[e] >= 0 ? __ldg(table + page_index(a, pos[e])) : -1;
           }
+          look(i + 1);
           ok = mbar_wait_bounded(&empty[stage], phase ^ 1, &abort_flag, &g_kv4_err);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
@@ -368,31 +433,31 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
           }
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
+            if (page[e] < 0 || page[e] >= a.c.n_pages) page[e] = pos[e] = -1;
             const int64_t blk = max(page[e], 0) * a.c.page_stride;
-            const int64_t off = pos[e] >= 0 ? blk + slot[e] * kKvCodeBytes : -1;
-            if (32 * e + lane < kBlock) st.pos[32 * e + lane] = pos[e];
+            const int slot = pos[e] >= 0 ? pos[e] - page_index(a, pos[e]) * a.c.page_size : 0;
+            const int64_t off = pos[e] >= 0 ? blk + slot * kKvCodeBytes : -1;
+            st.pos[32 * e + lane] = pos[e];
             if (pos[e] >= 0) {
-              cp_async4(&st.ks[32 * e + lane], kp + blk + scales_at + slot[e] * kKvScaleBytes);
-              cp_async4(&st.vs[32 * e + lane], vp + blk + scales_at + slot[e] * kKvScaleBytes);
+              const int to = kBlock * kKvCodeBytes + (32 * e + lane) * kKvScaleBytes;
+              cp_async4(st.k + to, kp + blk + scales_at + slot * kKvScaleBytes);
+              cp_async4(st.v + to, vp + blk + scales_at + slot * kKvScaleBytes);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {  // four lanes an entry's 64 bytes
               const int x = 8 * r + (lane >> 2);
               const int64_t o = __shfl_sync(0xffffffffu, off, x);
-              if (o < 0) continue;
-              cp_async16(st.k + (32 * e + x) * kKvCodeBytes + 16 * (lane & 3), kp + o + 16 * (lane & 3));
-              cp_async16(st.v + (32 * e + x) * kKvCodeBytes + 16 * (lane & 3), vp + o + 16 * (lane & 3));
+              if (o >= 0) {
+                cp_async16(st.k + (32 * e + x) * kKvCodeBytes + 16 * (lane & 3), kp + o + 16 * (lane & 3));
+                cp_async16(st.v + (32 * e + x) * kKvCodeBytes + 16 * (lane & 3), vp + o + 16 * (lane & 3));
+              }
             }
           }
           cp_async_arrive(&full[stage]);
           mbar_arrive(&full[stage]);
         } else {
-          // `run` tokens of a page lie together: a lane a run
-          const int at = n + lane * a.run;
-          const bool in = lane * a.run < kBlock && at < wk.rg.to;
-          const int pg = in ? page_index(a, at) : 0;
-          const int page = in ? __ldg(table + pg) : -1;
-          const int slot = at - pg * a.c.page_size;
+          const int page = ahead[0];
+          look(i + 1);
           const bool there = page >= 0 && page < a.c.n_pages;
           const uint32_t runs = __ballot_sync(0xffffffffu, there);
           const uint32_t chunks = __ballot_sync(0xffffffffu, lane * 16 < kBlock && ((runs >> (lane * 16 / a.run)) & 1u));
@@ -407,12 +472,20 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
           }
           __syncwarp();
           if (there) {
+            const int at = n + lane * a.run, slot = at - page_index(a, at) * a.c.page_size;
             const int64_t blk = page * a.c.page_stride;
-            const int to = lane * a.run;
-            bulk_g2s(st.k + to * kKvCodeBytes, kp + blk + slot * kKvCodeBytes, a.run * kKvCodeBytes, &full[stage]);
-            bulk_g2s(st.v + to * kKvCodeBytes, vp + blk + slot * kKvCodeBytes, a.run * kKvCodeBytes, &full[stage]);
-            bulk_g2s(st.ks + to, kp + blk + scales_at + slot * kKvScaleBytes, a.run * kKvScaleBytes, &full[stage]);
-            bulk_g2s(st.vs + to, vp + blk + scales_at + slot * kKvScaleBytes, a.run * kKvScaleBytes, &full[stage]);
+            uint8_t* ks = st.k + lane * a.run * kKvBytes;
+            uint8_t* vs = st.v + lane * a.run * kKvBytes;
+            if (a.run == a.c.page_size) {
+              bulk_g2s(ks, kp + blk, a.run * kKvBytes, &full[stage]);
+              bulk_g2s(vs, vp + blk, a.run * kKvBytes, &full[stage]);
+            } else {
+              const int codes = a.run * kKvCodeBytes, scales = a.run * kKvScaleBytes;
+              bulk_g2s(ks, kp + blk + slot * kKvCodeBytes, codes, &full[stage]);
+              bulk_g2s(vs, vp + blk + slot * kKvCodeBytes, codes, &full[stage]);
+              bulk_g2s(ks + codes, kp + blk + scales_at + slot * kKvScaleBytes, scales, &full[stage]);
+              bulk_g2s(vs + codes, vp + blk + scales_at + slot * kKvScaleBytes, scales, &full[stage]);
+            }
           }
         }
         filled |= 1u << stage;
@@ -433,16 +506,22 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
   const int g = lane >> 2, t = lane & 3;
   const int tk = (g >> 1) + 4 * (g & 1);  // the token of key row g (row g + 8: + 8)
   const int grp = g >> 1;                 // the scale group of dims 16g ..
-  int slot = 0;                           // of the segment's partial result
+  const bool bent = a.softcap > 0.f || a.slopes;
+  uint32_t blocks_done = 0;               // of the segments before
+  int slot = 0;                           // of the segment's partial result: 0 if the range begins with it
   bool ok = true;
-  for (; wk.w < wk.end; wk.next(a), wk.segment()) {
+  for (; wk.more(); wk.next(a)) {
+    if (wk.i0 == wk.i1) {
+      slot = 1;
+      continue;
+    }
     const Range& rg = wk.rg;
     const bool complete = wk.i0 == 0 && wk.i1 == rg.blocks;
     const int kh = wk.unit / a.row_tiles, r0 = (wk.unit - kh * a.row_tiles) * kRows;
     const int rows = min(kRows, a.Tq * G - r0), len = rg.len;
     const int p_first = len - a.Tq + r0 / G, p_last = len - a.Tq + (r0 + rows - 1) / G;
     const auto low_of = [&](int p) { return a.window > 0 ? max(rg.start, p - a.window + 1) : rg.start; };
-    const int lo_last = low_of(p_last);
+    const int lo_first = low_of(p_first), lo_last = low_of(p_last);
 
     // the queries: row g of each tile, dims 32t .. 32t+31, as f16 pieces of q * 2^-e, |.| < 2^8
     uint32_t qf[kQReg ? P : 1][8][2];
@@ -504,44 +583,45 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
     }
     if constexpr (!kQReg) named_barrier<32 * kWarps>();
 
-    float o[NT][8][4], M[NT][2], l[NT][2];
+    // the running maximum is kLift - base; lim is -infinity until the row has seen something
+    float o[NT][8][4], base[NT][2], lim[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.f;
-      M[nt][0] = M[nt][1] = kNoMax;
+      base[nt][0] = base[nt][1] = 0.f;
+      lim[nt][0] = lim[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // One tile.  FAST: every row sees all its tokens, and the scales are within f16's range (fast_scales).
-    const auto tile = [&](auto fast_c, const St& st, int j0, uint32_t there) {
-      constexpr bool FAST = decltype(fast_c)::value;
-      const int at = warp * kTok;  // the tile in the stage
-      const uint8_t* kc = st.k + at * kKvCodeBytes + tk * kKvCodeBytes + 16 * t;
-      const uint8_t* vc = st.v + at * kKvCodeBytes + t * kKvCodeBytes + 8 * g;
-      const uint32_t* ksp = st.ks + at + tk;
-      const uint32_t* vsp = st.vs + at + t;
+    // One tile.  FAST: its scales are within f16's range (fast_scales).  WHOLE: every row sees all its tokens.
+    const auto tile = [&](auto fast_c, auto whole_c, const St& st, int in_stage, const int4 pl, int j0, uint32_t there) {
+      constexpr bool FAST = decltype(fast_c)::value, WHOLE = decltype(whole_c)::value;
+      const int at = in_stage * kTok;
+      const int codes[2] = {pl.x, pl.z}, scales[2] = {pl.y, pl.w};  // of its halves
+      const auto k_scales = [&](int h, int k) {  // of the key of token k of half h
+        return *reinterpret_cast<const uint32_t*>(st.k + scales[h] + k * kKvScaleBytes);
+      };
+      const auto v_scales = [&](int h, int k) {
+        return *reinterpret_cast<const uint32_t*>(st.v + scales[h] + k * kKvScaleBytes);
+      };
       // position of token k of the tile, -1 where none is
       const auto pos_at = [&](int k) { return LIST ? st.pos[at + k] : (there >> (k >> 4)) & 1u ? j0 + k : -1; };
       // ---- scores: S[token][row] = K q^T
       float s[H][NT][4];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[h][nt][c] = 0.f;
         uint32_t f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t w = ksp[16 * h + 8 * i];
+          const uint32_t w = k_scales(h, 8 * i + tk);
           if constexpr (FAST) f[i] = fast_factor(__byte_perm(w, 0, 0x4040 + 0x0101 * t));
           else f[i] = group_factor(w, t, top_scale(w)) * 0x10001u;
         }
-        const uint4 k0 = *reinterpret_cast<const uint4*>(kc + 16 * h * kKvCodeBytes);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(kc + (16 * h + 8) * kKvCodeBytes);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(st.k + codes[h] + tk * kKvCodeBytes + 16 * t);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(st.k + codes[h] + (8 + tk) * kKvCodeBytes + 16 * t);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -557,12 +637,10 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int p = 0; p < P; ++p) {
-                if constexpr (kQReg) {
-                  mma_f16(s[h][nt], A, qf[p][j][0], qf[p][j][1]);
-                } else {
-                  const uint2 q2 = sq[((nt * P + p) * 8 + j) * 32 + lane];
-                  mma_f16(s[h][nt], A, q2.x, q2.y);
-                }
+                const uint2 q2 = kQReg ? make_uint2(qf[kQReg ? p : 0][j][0], qf[kQReg ? p : 0][j][1])
+                                       : sq[((nt * P + p) * 8 + j) * 32 + lane];
+                if (j == 0 && p == 0) mma_f16_zero(s[h][nt], A, q2.x, q2.y);
+                else mma_f16(s[h][nt], A, q2.x, q2.y);
               }
           }
         }
@@ -574,9 +652,9 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
         for (int h = 0; h < H; ++h)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = ksp[16 * h + 8 * i], r = top_scale(w);
+            const uint32_t w = k_scales(h, 8 * i + tk), r = top_scale(w);
             k_top[h][i] = has_nan(w) ? nan_f32() : e8m0_value(r);
-            const uint32_t rv = top_value_scale(st.vs[at + 16 * h + 8 * i + tk]);
+            const uint32_t rv = top_value_scale(v_scales(h, 8 * i + tk));
             v_exp[h][i] = (float)((int)rv - 127);
             v_inv[h][i] = rv < 254u ? __uint_as_float((254u - rv) << 23) : 0.5f * kMinNormal;
           }
@@ -584,52 +662,70 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
       uint32_t pf[H][NT][P][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float u[H][4];  // [half][c]: tokens tk, tk, tk + 8, tk + 8; columns 2t, 2t + 1, 2t, 2t + 1
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            u[h][c] = s[h][nt][c] * (FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1]);
-        if (a.softcap > 0.f) {  // coef holds scale / softcap: cap * tanh(x) = cap - 2 cap / (1 + e^2x)
+        // x: log2 of the weights, relative to the running maximum and times 2^kLift.  [half][c]: tokens tk, tk,
+        // tk + 8, tk + 8; columns 2t, 2t + 1, 2t, 2t + 1
+        float x[H][4];
+        if (!bent) {
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              u[h][c] = a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(u[h][c] * (2.f * kLog2e)));
-        }
-        if (a.slopes) {
+              x[h][c] = fmaf(s[h][nt][c], FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1], base[nt][c & 1]);
+        } else {
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              u[h][c] = fmaf(slope[nt][c & 1], (float)(pos_at(16 * h + 8 * (c >> 1) + tk) - pq[nt][c & 1]), u[h][c]);
+            for (int c = 0; c < 4; ++c) {
+              float y = s[h][nt][c] * (FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1]);
+              if (a.softcap > 0.f)  // coef holds scale / softcap: cap * tanh(y) = cap - 2 cap / (1 + e^2y)
+                y = a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(y * (2.f * kLog2e)));
+              if (a.slopes)
+                y = fmaf(slope[nt][c & 1], (float)(pos_at(16 * h + 8 * (c >> 1) + tk) - pq[nt][c & 1]), y);
+              x[h][c] = y + base[nt][c & 1];
+            }
         }
         if constexpr (!FAST) {
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
+            for (int c = 0; c < 4; ++c) x[h][c] += v_exp[h][c >> 1];
+        }
+        if constexpr (!WHOLE) {
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int j = pos_at(16 * h + 8 * (c >> 1) + tk), p = pq[nt][c & 1];
-              u[h][c] = j > p || j < low_of(p) ? -INFINITY : u[h][c] + v_exp[h][c >> 1];
+              if (j > p || j < low_of(p)) x[h][c] = -INFINITY;
             }
         }
+        // the maximum moves only where a weight would pass 2^(kLift + kLazy), or at what a row sees first
+        float m[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(u[0][i], u[0][i + 2]);
-          if constexpr (H == 2) m = fmaxf(m, fmaxf(u[1][i], u[1][i + 2]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          const bool up = m > M[nt][i] + kLazy;
-          if (__any_sync(0xffffffffu, up)) {
-            const float mn = up ? m : M[nt][i];
-            const float f = ex2(M[nt][i] - mn);
-            M[nt][i] = mn;
-            l[nt][i] *= f;
+        for (int i = 0; i < 2; ++i) m[i] = fmaxf(fmaxf(x[0][i], x[0][i + 2]), fmaxf(x[1][i], x[1][i + 2]));
+        if (__any_sync(0xffffffffu, m[0] > lim[nt][0] || m[1] > lim[nt][1])) {
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              o[nt][d][i] *= f;
-              o[nt][d][i + 2] *= f;
+          for (int i = 0; i < 2; ++i) {
+            float top = m[i];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (top > lim[nt][i]) {
+              const float down = top - kLift;
+              const float f = lim[nt][i] == -INFINITY ? 0.f : ex2(-down);  // a row's first: there is nothing to rescale
+              base[nt][i] -= down;
+              lim[nt][i] = kLift + kLazy;
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                x[h][i] -= down;
+                x[h][i + 2] -= down;
+              }
+              l[nt][i] *= f;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[nt][d][i] *= f;
+                o[nt][d][i + 2] *= f;
+              }
             }
           }
         }
@@ -638,7 +734,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
           float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            w[c] = ex2(u[h][c] - (M[nt][c & 1] - kLift));
+            w[c] = ex2(x[h][c]);
             l[nt][c & 1] = FAST ? l[nt][c & 1] + w[c] : fmaf(w[c], v_inv[h][c >> 1], l[nt][c & 1]);
           }
 #pragma unroll
@@ -654,9 +750,10 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
       }
       if constexpr (!FAST) {
         // a NaN scale makes its dimensions NaN for the rows that see the token, and for no other
+        const uint32_t nans = __ballot_sync(0xffffffffu, has_nan(lane < 16 ? v_scales(0, lane) : v_scales(1, lane - 16)));
 #pragma unroll 1
         for (int k = 0; k < kTok; ++k) {
-          if (byte_of(st.vs[at + k], grp) != 255u) continue;
+          if (!((nans >> k) & 1u) || byte_of(k < 16 ? v_scales(0, k) : v_scales(1, k - 16), grp) != 255u) continue;
           const int j = pos_at(k);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -673,10 +770,10 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
         uint32_t f[2];  // factors of tokens (t, t + 4) and (t + 8, t + 12) for dims 16g ..
         uint2 vr[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vr[i] = *reinterpret_cast<const uint2*>(vc + (16 * h + 4 * i) * kKvCodeBytes);
+        for (int i = 0; i < 4; ++i) vr[i] = *reinterpret_cast<const uint2*>(st.v + codes[h] + (4 * i + t) * kKvCodeBytes + 8 * g);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t wa = vsp[16 * h + 8 * i], wb = vsp[16 * h + 8 * i + 4];
+          const uint32_t wa = v_scales(h, 8 * i + t), wb = v_scales(h, 8 * i + 4 + t);
           if constexpr (FAST) {
             f[i] = fast_factor(__byte_perm(wa, wb, 0x4400 + 0x1111 * grp) & 0x00ff00ffu);
           } else {
@@ -706,57 +803,87 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
         }
       }
     };
-    for (int i = wk.i0; i < wk.i1; ++i) {
-      const St& st = stages[stage];
-      const int j0 = rg.from + i * kBlock + warp * kTok;  // the tile's first token (list: entry)
+    const int n_tiles = (wk.i1 - wk.i0) * kTiles;
+    for (int tile_at = warp; tile_at < n_tiles;) {
+      uint32_t after = 0;
+      if (lane == 0) after = atomicAdd(&next_tile, 1u);
+      const uint32_t blk = blocks_done + (uint32_t)(tile_at / kTiles), stage = blk % kStages;
+      const int in_stage = tile_at % kTiles;
+      St& st = ring[stage];
+      const int j0 = rg.from + wk.i0 * kBlock + tile_at * kTok;  // the tile's first token (list: entry)
       // a wait that ran out ends the work, not the walk: the barriers below want every warp
-      if (ok) ok = mbar_wait_bounded(&full[stage], phase, &abort_flag, &g_kv4_err);
+      if (ok) ok = mbar_wait_bounded(&full[stage], (blk / kStages) & 1u, &abort_flag, &g_kv4_err);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
-        const uint32_t kw = st.ks[warp * kTok + (lane & (kTok - 1))], vw = st.vs[warp * kTok + (lane & (kTok - 1))];
-        const uint32_t there = LIST ? 0u : (st.there >> (warp * H)) & ((1u << H) - 1u);
-        bool mine = fast_scales(kw) && fast_scales(vw);
-        bool any;  // some row may see something
+        const int4 pl = place[in_stage];
+        const int mine = (lane < 16 ? pl.y : pl.w) + (lane & 15) * kKvScaleBytes;  // the scales of this lane's token
+        uint32_t kw = *reinterpret_cast<const uint32_t*>(st.k + mine), vw = *reinterpret_cast<const uint32_t*>(st.v + mine);
+        const uint32_t there = LIST ? 0u : st.there >> (in_stage * H);
+        bool whole, any = true;
         if constexpr (LIST) {
-          const int j = st.pos[warp * kTok + (lane & (kTok - 1))];
-          mine = mine && j >= lo_last && j <= p_first;
-          any = j0 < rg.to;
+          const int j = st.pos[in_stage * kTok + lane];
+          whole = __all_sync(0xffffffffu, j >= lo_last && j <= p_first);
         } else {
-          mine = mine && j0 >= lo_last && j0 + kTok - 1 <= p_first && there == (1u << H) - 1u;
-          any = j0 <= p_last && there != 0u;
+          whole = j0 >= lo_last && j0 + kTok - 1 <= p_first && (there & 3u) == 3u;
         }
-        if (__all_sync(0xffffffffu, mine)) tile(std::true_type{}, st, j0, there);
-        else if (any) tile(std::false_type{}, st, j0, there);
+        if (!whole) {
+          // what no row sees may hold anything: its scales are made harmless
+          const int j = LIST ? st.pos[in_stage * kTok + lane] : (there >> (lane >> 4)) & 1u ? j0 + lane : -1;
+          const bool seen = j >= lo_first && j <= p_last;
+          if (!seen) {
+            kw = vw = 0x7f7f7f7fu;
+            *reinterpret_cast<uint32_t*>(st.k + mine) = kw;
+            *reinterpret_cast<uint32_t*>(st.v + mine) = vw;
+          }
+          any = __any_sync(0xffffffffu, seen);
+          fence_proxy_async_smem();  // the stage's next copy comes after these
+          __syncwarp();
+        }
+        const bool fast = __all_sync(0xffffffffu, fast_scales(kw, vw));
+        if (any) {
+          if (!fast) tile(std::false_type{}, std::false_type{}, st, in_stage, pl, j0, there);
+          else if (whole) tile(std::true_type{}, std::true_type{}, st, in_stage, pl, j0, there);
+          else tile(std::true_type{}, std::false_type{}, st, in_stage, pl, j0, there);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
       }
-      advance();
+      tile_at = (int)__shfl_sync(0xffffffffu, after, 0);
     }
+    blocks_done += (uint32_t)(wk.i1 - wk.i0);
 
-    // ---- the warps' sums merged in shared memory: those from 4 on add to the first ones, then those from 2 on, then the second
+    // ---- the warps' sums merged in shared memory: two at a time add to the first two, then the second to the first
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
+    float M[NT][2];  // the maxima less kLift, which all sums have
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) M[nt][i] = lim[nt][i] == -INFINITY ? kNoMax : -base[nt][i];
+    const auto put = [&](int to) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
+          float* row = so + (to * kRows + r) * kORow;
+#pragma unroll
+          for (int d = 0; d < 8; ++d)  // dims 16g + 2d, + 1 at 16d + 2g, + 1
+            *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[nt][d][i], o[nt][d][i + 2]);
+          if (g == 0) sml[to][r] = make_float2(M[nt][i], l[nt][i]);
+        }
+    };
 #pragma unroll 1
-    for (int half = 4; half > 0; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = nt * 8 + 2 * t + i;
-            float* row = so + ((warp - half) * kRows + r) * kORow;
-#pragma unroll
-            for (int d = 0; d < 8; ++d)  // dims 16g + 2d, + 1 at 16d + 2g, + 1
-              *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[nt][d][i], o[nt][d][i + 2]);
-            if (g == 0) sml[warp - half][r] = make_float2(M[nt][i], l[nt][i]);
-          }
-      }
+    for (int left = kWarps; left > 1;) {
+      const int n_from = left > 3 ? 2 : 1;
+      left -= n_from;
+      if (warp >= left && warp < left + n_from) put(warp - left);
       named_barrier<32 * kWarps>();
-      if (warp < half && warp + half < kWarps) {
+      if (warp < n_from) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -777,20 +904,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
       }
       named_barrier<32 * kWarps>();
     }
-    // the first warp has the sums; all of them write them out
-    if (warp == 0) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = nt * 8 + 2 * t + i;
-          float* row = so + r * kORow;
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-            *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[nt][d][i], o[nt][d][i + 2]);
-          if (g == 0) sml[0][r] = make_float2(M[nt][i], l[nt][i]);
-        }
-    }
+    if (warp == 0) put(0);  // all of them write it out
     named_barrier<32 * kWarps>();
     for (int x = threadIdx.x; x < rows * kKvDim; x += 32 * kWarps) {
       const int r = x / kKvDim, d = x % kKvDim;
@@ -804,6 +918,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, Shape<NT, P>::kCtas) k
       }
     }
     slot = 1;
+    if (threadIdx.x == 0) next_tile = kWarps;
     named_barrier<32 * kWarps>();  // the shared memory is used again
   }
 }
@@ -891,7 +1006,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Attn
 // times blocks of tokens, shared evenly by as many CTAs as the GPU holds at once,
 // however the rows' lengths differ.
 struct AttnPlan {
-  int nt, row_tiles, block, grid;
+  int nt, row_tiles, grid;
   bool wide;  // few units: each is shared by many CTAs
 };
 
@@ -899,15 +1014,14 @@ constexpr int kSms = 148;
 
 AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   AttnPlan p;
-  const int rows = d->Tq * (d->n_q_heads / c->n_kv_heads), pieces = d->dtype == FM_F32 ? 2 : 1;
-  p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const int rows = d->Tq * (d->n_q_heads / c->n_kv_heads);
+  p.nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
   int64_t tokens = d->idx ? d->max_sel : d->max_len;
-  if (!d->idx && d->window > 0)  // a row reaches back window + Tq - 1 from the last token, from a multiple of 32
-    tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kMaxRunTok - 1);
+  if (!d->idx && d->window > 0)  // a row reaches back window + Tq - 1 from the last token, from a multiple of 128
+    tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kBlock - 1);
   const int64_t units = (int64_t)c->B * c->n_kv_heads * p.row_tiles;
-  p.block = block_tokens(p.nt, pieces);
-  p.grid = (int)std::min<int64_t>(units * ((tokens + p.block - 1) / p.block), kSms * ctas_per_sm(p.nt));
+  p.grid = (int)std::min<int64_t>(units * ((tokens + kBlock - 1) / kBlock), kSms * kCtas);
   p.wide = 8 * units <= p.grid;
   return p;
 }
@@ -966,10 +1080,9 @@ namespace {
 template <class T, int NT, int P, bool LIST>
 fm_status launch_attn(const AttnArgs& a, int grid, cudaStream_t stream) {
   using S = Shape<NT, P>;
-  static_assert(S::kBlock == block_tokens(NT, P) && S::kCtas == ctas_per_sm(NT), "the host's plan is the kernel's");
-  constexpr int kSmem = S::kStages * (int)sizeof(Stage<S::kBlock>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
-                        S::kMergers * S::kRows * kORow * (int)sizeof(float);
-  static_assert(kSmem * S::kCtas <= 225 * 1024, "shared memory of an SM");
+  constexpr int kSmem = stages(NT, LIST) * (int)sizeof(Stage<LIST>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
+                        2 * S::kRows * kORow * (int)sizeof(float);
+  static_assert((kSmem + 2048) * kCtas <= 228 * 1024, "shared memory of an SM, with the static and the reserved parts");
   static PerDeviceOnce once;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -983,8 +1096,7 @@ template <class T, bool LIST>
 fm_status launch_attn_nt(const AttnArgs& a, int nt, int grid, cudaStream_t stream) {
   constexpr int P = sizeof(T) == 4 ? 2 : 1;
   if (nt == 1) return launch_attn<T, 1, P, LIST>(a, grid, stream);
-  if (nt == 2) return launch_attn<T, 2, P, LIST>(a, grid, stream);
-  return launch_attn<T, 4, P, LIST>(a, grid, stream);
+  return launch_attn<T, 2, P, LIST>(a, grid, stream);
 }
 
 }  // namespace
@@ -1022,7 +1134,7 @@ extern "C" fm_status fm_kv4_attention(const fm_kv4_cache* c, const fm_kv4_attn_d
   const int q16 = c->page_size / 16;
   a.page_magic = q16 == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q16 - 1) / q16);
   a.row_tiles = p.row_tiles;
-  a.run = std::min(c->page_size & -c->page_size, p.nt == 4 ? 16 : kMaxRunTok);
+  a.run = d->idx ? kBlock : std::min(c->page_size & -c->page_size, kBlock);
   uint8_t* at = static_cast<uint8_t*>(ws);
   a.share = reinterpret_cast<Share*>(at);
   a.part_ml = reinterpret_cast<float2*>(at + sp.share);
