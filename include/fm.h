@@ -510,8 +510,9 @@ fm_status fm_rope_frequencies(const fm_config* cfg, double* inv_freq_host);
  *
  * Rotation: half-split pairs of the last rope_dim dimensions, as query prep
  * does it: x1' = x1 c - x2 s, x2' = x2 c + x1 s with c, s = fp32(cos, sin of
- * the fp64 angle positions[t] * inv_freq[j]).  The products and their sum are
- * exact to 2^-46 before the one rounding to the code (or to q_out's type). */
+ * the fp64 angle positions[t] * inv_freq[j]).  A key's products and their sum
+ * are exact to 2^-46 before the one rounding to its code, and a query's before
+ * the one to fp32; a 16-bit query is rounded from within 1.5 units of fp32. */
 typedef struct fm_kv4_append_desc {
   int dtype;                  /* FM_F32, FM_BF16, FM_F16: of k, v, q and q_out */
   int T;                      /* tokens, >= 1 */
@@ -604,15 +605,16 @@ fm_status fm_index_append(const void* k, int dtype, int64_t token_stride, int T,
  * (fm_toy_decoder_update with a gain, the model's types and a narrow output).
  *   z = x + residual (fp32; residual NULL: x);  sum_out = z in the type
  *   y = z * (mean(z^2) + eps)^-1/2 * gain (gain NULL: 1)
- *   scale[t, g] = max|y| over group g / 448;  codes = e4m3(y * (1 / scale))
- * A group whose scale would be below 2^-126 is stored as zeros with scale 0; a
- * row whose sum of squares is not finite in fp32 (a NaN, an infinity, values
- * past 2^63) has NaN scales.
+ *   scale[t, g] = max|y| over group g / 448;  codes = e4m3(y / scale)
+ * (formed as z * gain * (448 / max|z * gain|), in fp32).  A group whose largest
+ * |z * gain| is below 2^-100 is stored as zeros with scale 0; a row whose sum of
+ * squares is not finite in fp32 (a NaN, an infinity, values past 2^63) has NaN
+ * scales.
  * x, residual [T, H] device, 16-byte aligned, x_stride / residual_stride elements between rows (times
  * the element size: a multiple of 16); gain [H] of the same type; sum_out
  * [T, H] packed or NULL, may be x or residual when that is packed; codes
  * [T, H] packed; scales [T, H / group] fp32.  H a multiple of 128, at most
- * 65536; group 128 or H. */
+ * 32768; group 128 or H. */
 fm_status fm_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
                              const void* gain, int dtype, int T, int H, float eps, int group, void* sum_out,
                              uint8_t* codes, float* scales, cudaStream_t stream);

@@ -1,94 +1,134 @@
 // add_rmsnorm.cu -- residual addition, RMSNorm and an e4m3 output with scales
 // (fm_add_rmsnorm_fp8).
+//
+// Mathematics.  With t = z * gain a group's scale is max|t| * rms^-1 / 448 and its
+// codes are t * 448 / max|t|: the row's mean of squares only enters the scales,
+// so the codes are formed from the groups' maxima while the row's sum is still
+// under way, and with one scale a row the sum and the maximum are reduced
+// together.  Bound by memory: x and the residual are read once (16 bytes a
+// thread and load, all of a row's loads in flight before the first use), z stays
+// in registers as fp32, and the sum, the codes and the scales are written once.
 #include <cmath>
+#include <type_traits>
 
 #include "kv4.cuh"
 
 namespace fm {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
+constexpr int kNormVecs = 4;      // vectors of 8 elements a thread keeps
+constexpr int kNormMaxH = 32768;  // 1024 threads of kNormVecs vectors
 
 struct NormArgs {
   const void* x;
   const void* residual;
   const void* gain;
   int64_t x_stride, r_stride;
-  int H, group;
+  int T, H;
   float eps;
   void* sum_out;
   uint8_t* codes;
   float* scales;
 };
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float r = 0.f;
-#pragma unroll
-  for (int i = 0; i < kNormThreads / 32; ++i) r += red[i];
-  return r;
-}
-
-// One CTA a row, three passes: the sum of squares, the groups' maxima, the codes.
-template <class T>
-__global__ void __launch_bounds__(kNormThreads) add_rmsnorm_simple_kernel(const NormArgs a) {
-  __shared__ float red[kNormThreads / 32];
-  const int64_t t = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
-  const T* r = a.residual ? static_cast<const T*>(a.residual) + t * a.r_stride : nullptr;
+// TPR threads a row (a power of two from 16 on), blockDim.x / TPR rows a CTA.
+// PER_ROW: one scale for the row.
+template <class T, int TPR, bool PER_ROW>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(const NormArgs a) {
+  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+  constexpr int kWarps = TPR < 32 ? 1 : TPR / 32;  // that share a row
+  __shared__ float2 red[kRows * kWarps];
+  const int lane = threadIdx.x & 31, at = threadIdx.x % TPR, vecs = a.H / 8;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  const bool in = row < a.T;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const T* r = static_cast<const T*>(a.residual) + row * a.r_stride;
   const T* gain = static_cast<const T*>(a.gain);
-  const auto z_at = [&](int i) { return load1(x + i) + (r ? load1(r + i) : 0.f); };
-  float ss = 0.f;
-  for (int i = threadIdx.x; i < a.H; i += kNormThreads) {
-    const float z = z_at(i);
-    ss = fmaf(z, z, ss);
+  float z[kNormVecs][8];
+#pragma unroll
+  for (int v = 0; v < kNormVecs; ++v) {
+    const int i = at + v * TPR;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[v][k] = 0.f;
+    if (in && i < vecs) load8(x + 8 * i, z[v]);
   }
-  const float ms = block_sum(ss, red) / (float)a.H + a.eps;
+  if (a.residual) {
+#pragma unroll
+    for (int v = 0; v < kNormVecs; ++v) {
+      const int i = at + v * TPR;
+      if (in && i < vecs) {
+        float y[8];
+        load8(r + 8 * i, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[v][k] += y[k];
+      }
+    }
+  }
+  // the sum of squares; z stored, then turned into t
+  float ss = 0.f, top[kNormVecs], row_top = 0.f;
+#pragma unroll
+  for (int v = 0; v < kNormVecs; ++v) {
+    const int i = at + v * TPR;
+    top[v] = 0.f;
+    if (!(in && i < vecs)) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = fmaf(z[v][k], z[v][k], ss);
+    if (a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.H + 8 * i, z[v]);
+    if (a.gain) {
+      float w[8];
+      load8(gain + 8 * i, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z[v][k] *= w[k];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top[v] = fmax_nan(top[v], fabsf(z[v][k]));
+    row_top = fmax_nan(row_top, top[v]);
+  }
+#pragma unroll
+  for (int d = 1; d < (TPR < 32 ? TPR : 32); d <<= 1) {
+    ss += __shfl_xor_sync(0xffffffffu, ss, d);
+    if (PER_ROW) row_top = fmax_nan(row_top, __shfl_xor_sync(0xffffffffu, row_top, d));
+  }
+  if constexpr (!PER_ROW) {  // 16 lanes a group
+#pragma unroll
+    for (int v = 0; v < kNormVecs; ++v)
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) top[v] = fmax_nan(top[v], __shfl_xor_sync(0xffffffffu, top[v], d));
+  }
+  if constexpr (kWarps > 1) {
+    if (lane == 0) red[threadIdx.x >> 5] = make_float2(ss, row_top);
+    __syncthreads();
+    const float2 w = red[(threadIdx.x / TPR) * kWarps + (lane < kWarps ? lane : 0)];
+    ss = lane < kWarps ? w.x : 0.f;
+    row_top = w.y;
+#pragma unroll
+    for (int d = 1; d < kWarps; d <<= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      if (PER_ROW) row_top = fmax_nan(row_top, __shfl_xor_sync(0xffffffffu, row_top, d));
+    }
+    ss = __shfl_sync(0xffffffffu, ss, 0);
+    row_top = __shfl_sync(0xffffffffu, row_top, 0);
+  }
+  if (!in) return;
+  const float ms = ss / (float)a.H + a.eps;
   const float inv_rms = ms < INFINITY ? rsqrtf(ms) : nan_f32();
-  const auto y_at = [&](int i) { return z_at(i) * inv_rms * (gain ? load1(gain + i) : 1.f); };
-  const int lane = threadIdx.x & 31;
-  float row_max = 0.f;
-  if (a.group != kKvDim) {
-    for (int i = threadIdx.x; i < a.H; i += kNormThreads) row_max = fmax_nan(row_max, fabsf(y_at(i)));
+  constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100: below it a group is stored as zeros
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) row_max = fmax_nan(row_max, __shfl_xor_sync(0xffffffffu, row_max, s));
-    __syncthreads();
-    if (lane == 0) red[threadIdx.x >> 5] = row_max;
-    __syncthreads();
-    for (int i = 0; i < kNormThreads / 32; ++i) row_max = fmax_nan(row_max, red[i]);
-  }
-  // a warp a group of 128: four elements a lane
-  for (int g = threadIdx.x >> 5; g < a.H / kKvDim; g += kNormThreads / 32) {
-    float y[4], z[4], m = row_max;
+  for (int v = 0; v < kNormVecs; ++v) {
+    const int i = at + v * TPR;
+    if (i >= vecs) continue;
+    const float m = PER_ROW ? row_top : top[v];
+    const float up = m < kTiny ? 0.f : 448.f / m;
+    uint32_t c[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      z[k] = z_at(g * kKvDim + 4 * lane + k);
-      y[k] = y_at(g * kKvDim + 4 * lane + k);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(z[v][4 * k] * up, z[v][4 * k + 1] * up), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z[v][4 * k + 2] * up, z[v][4 * k + 3] * up), __NV_SATFINITE, __NV_E4M3);
+      c[k] = lo | (hi << 16);
     }
-    if (a.group == kKvDim) {
-      m = fmax_nan(fmax_nan(fabsf(y[0]), fabsf(y[1])), fmax_nan(fabsf(y[2]), fabsf(y[3])));
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
-    }
-    float scale = m / 448.f;
-    const float inv = scale >= kMinNormal ? 1.f / scale : 0.f;
-    if (scale < kMinNormal) scale = 0.f;
-    if (!(scale < INFINITY)) scale = nan_f32();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t at = t * a.H + g * kKvDim + 4 * lane + k;
-      a.codes[at] = __nv_cvt_float_to_fp8(y[k] * inv, __NV_SATFINITE, __NV_E4M3);
-      if (a.sum_out) store1(static_cast<T*>(a.sum_out) + at, z[k]);
-    }
-    if (lane == 0) {
-      if (a.group == kKvDim) a.scales[t * (a.H / kKvDim) + g] = scale;
-      else if (g == 0) a.scales[t] = scale;
-    }
+    *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * i) = make_uint2(c[0], c[1]);
+    const float scale = m < kTiny ? 0.f * inv_rms : m * inv_rms * (1.f / 448.f);  // NaN where the row's sum is
+    if (PER_ROW ? i == 0 : (i & 15) == 0) a.scales[PER_ROW ? row : row * (a.H / kKvDim) + (i >> 4)] = scale;
   }
 }
 
@@ -104,7 +144,7 @@ extern "C" fm_status fm_add_rmsnorm_fp8(const void* x, int64_t x_stride, const v
                                         uint8_t* codes, float* scales, cudaStream_t stream) {
   if (!x || !codes || !scales || !dtype_ok(dtype) || T < 1 || H < 1 || !(eps >= 0.f) || !std::isfinite(eps))
     return FM_ERR_INVALID_ARG;
-  if (H % kKvDim || H > 65536 || (group != kKvDim && group != H)) return FM_ERR_UNSUPPORTED;
+  if (H % kKvDim || H > kNormMaxH || (group != kKvDim && group != H)) return FM_ERR_UNSUPPORTED;
   if (x_stride < H || (residual && residual_stride < H)) return FM_ERR_INVALID_ARG;
   if (sum_out && ((sum_out == x && x_stride != H) || (sum_out == residual && residual_stride != H)))
     return FM_ERR_INVALID_ARG;
@@ -112,11 +152,29 @@ extern "C" fm_status fm_add_rmsnorm_fp8(const void* x, int64_t x_stride, const v
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(sum_out) || !aligned16(codes) ||
       (x_stride * es) % 16 || (residual && (residual_stride * es) % 16) || (reinterpret_cast<uintptr_t>(scales) & 3u))
     return FM_ERR_ALIGNMENT;
-  NormArgs a = {x, residual, gain, x_stride, residual_stride, H, group, eps, sum_out, codes, scales};
-  return by_dtype(dtype, [&](auto* tag) {
+  NormArgs a = {x, residual, gain, x_stride, residual_stride, T, H, eps, sum_out, codes, scales};
+  // the fewest threads that hold a row
+  int tpr = 16;
+  while (tpr * 8 * kNormVecs < H) tpr *= 2;
+  return by_dtype(dtype, [&](auto* tag) -> fm_status {
     using E = std::remove_pointer_t<decltype(tag)>;
-    add_rmsnorm_simple_kernel<E><<<T, kNormThreads, 0, stream>>>(a);
-    note_launch();
-    return check_launch();
+    const auto go = [&](auto n) -> fm_status {
+      constexpr int TPR = decltype(n)::value;
+      constexpr int kThreads = TPR < 128 ? 128 : TPR;
+      const unsigned grid = (unsigned)(((int64_t)T + kThreads / TPR - 1) / (kThreads / TPR));
+      if (group == H && H != kKvDim) add_rmsnorm_kernel<E, TPR, true><<<grid, kThreads, 0, stream>>>(a);
+      else add_rmsnorm_kernel<E, TPR, false><<<grid, kThreads, 0, stream>>>(a);
+      note_launch();
+      return check_launch();
+    };
+    switch (tpr) {
+      case 16: return go(std::integral_constant<int, 16>{});
+      case 32: return go(std::integral_constant<int, 32>{});
+      case 64: return go(std::integral_constant<int, 64>{});
+      case 128: return go(std::integral_constant<int, 128>{});
+      case 256: return go(std::integral_constant<int, 256>{});
+      case 512: return go(std::integral_constant<int, 512>{});
+      default: return go(std::integral_constant<int, 1024>{});
+    }
   });
 }

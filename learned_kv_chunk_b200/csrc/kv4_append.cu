@@ -18,7 +18,9 @@
 //   * Scale: the least power of two 2^e with max|x| <= 6 * 2^e (6 is the
 //     largest e2m1 value), read from the exponent and mantissa bits of the
 //     group's maximum; x * 2^-e is exact.
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -28,10 +30,37 @@ namespace {
 constexpr int kAppThreads = 256;              // 16 heads of 16 lanes each
 constexpr int kAppUnits = kAppThreads / 16;
 
-// fp64 angle positions * f; cos and sin rounded to fp32 once, as query prep does.
+// cos and sin of the fp64 angle position * f, rounded to fp32 once, as query prep
+// does.  The angle less the nearest multiple n of pi/2 (two fused steps with pi/2
+// in two parts: exact to 2^-100 n), then the Taylor series of both functions to
+// x^17 and x^16, whose next terms are below 2^-58 for |x| <= pi/4.  Beyond 2^40 the
+// two parts of pi/2 would no longer do.
 __device__ __forceinline__ float2 rope_cos_sin(int64_t position, double f) {
+  const double x = (double)position * f;
   double s, c;
-  sincos((double)position * f, &s, &c);
+  if (fabs(x) < 1099511627776.0) {
+    const double n = rint(x * 0.63661977236758134308);  // 2 / pi
+    double r = fma(n, -1.57079632679489655800, x);
+    r = fma(n, -6.12323399573676603587e-17, r);
+    const double q = r * r;
+    // 1 / 17!, -1 / 15!, ... and 1 / 16!, -1 / 14!, ...
+    double a = 2.8114572543455206e-15, b = 4.7794773323873853e-14;
+    a = fma(a, q, -7.6471637318198164e-13); b = fma(b, q, -1.1470745597729725e-11);
+    a = fma(a, q, 1.6059043836821613e-10);  b = fma(b, q, 2.0876756987868099e-09);
+    a = fma(a, q, -2.5052108385441720e-08); b = fma(b, q, -2.7557319223985888e-07);
+    a = fma(a, q, 2.7557319223985893e-06);  b = fma(b, q, 2.4801587301587302e-05);
+    a = fma(a, q, -1.9841269841269841e-04); b = fma(b, q, -1.3888888888888889e-03);
+    a = fma(a, q, 8.3333333333333332e-03);  b = fma(b, q, 4.1666666666666664e-02);
+    a = fma(a, q, -1.6666666666666666e-01); b = fma(b, q, -0.5);
+    const double sn = fma(a * q, r, r), cn = fma(b, q, 1.0);
+    const int k = (int)((long long)n & 3);
+    s = (k & 1) ? cn : sn;
+    c = (k & 1) ? sn : cn;
+    if (k & 2) s = -s;
+    if (k == 1 || k == 2) c = -c;
+  } else {
+    sincos(x, &s, &c);
+  }
   return make_float2((float)c, (float)s);
 }
 
@@ -57,28 +86,44 @@ __device__ __forceinline__ void rot_pair(float a, float c, float b, float s, flo
   }
 }
 
+// a * c - b * s (NEG) or a * c + b * s within 1.5 units of fp32's last place,
+// whatever cancels: the second product's rounding is taken back.
+template <bool NEG>
+__device__ __forceinline__ float rot_near(float a, float c, float b, float s) {
+  const float bs = NEG ? -b : b;
+  const float q = __fmul_rn(bs, s);
+  return __fadd_rn(__fmaf_rn(a, c, q), __fmaf_rn(bs, s, -q));
+}
+
 // Rotates the lane's 8 values of a head (lane l of 16 has dims 8l .. 8l+7).
-// cs: cos, sin of the token for j < RD / 2.
-template <int RD>
-__device__ __forceinline__ void rotate8(float (&x)[8], float (&odd)[8], int l, const float2* cs) {
-  if constexpr (RD == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) odd[i] = x[i];
-  } else {
+// cs: cos, sin of the token for j < RD / 2.  How a value comes back: ODD rounded to
+// odd (codes, and whatever else rounds it again), FULL rounded to fp32, NEAR
+// within 1.5 units of fp32.
+enum RotMode { kRotOdd, kRotFull, kRotNear };
+template <int RD, RotMode MODE>
+__device__ __forceinline__ void rotate8(float (&x)[8], int l, const float2* cs) {
+  if constexpr (RD != 0) {
     constexpr int kHalfLanes = RD / 16;              // lanes of half a pair range
     constexpr int kFirst = (kKvDim - RD) / 8;        // first rotated lane
     const bool in = l >= kFirst;
     const bool second = in && l >= kFirst + kHalfLanes;
     const int j0 = in ? 8 * (second ? l - kFirst - kHalfLanes : l - kFirst) : 0;
+    float other[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, x[i], kHalfLanes);
-      const float2 w = cs[j0 + i];
-      float hi, o;
-      if (second) rot_pair<false>(x[i], w.x, other, w.y, hi, o);
-      else rot_pair<true>(x[i], w.x, other, w.y, hi, o);
-      odd[i] = in ? o : x[i];
-      x[i] = in ? hi : x[i];
+    for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, x[i], kHalfLanes);
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 w = cs[j0 + i];
+        const float s = second ? -w.y : w.y;  // x1 c - x2 s, and x2 c - x1 (-s)
+        if (MODE == kRotNear) {
+          x[i] = rot_near<true>(x[i], w.x, other[i], s);
+        } else {
+          float hi, odd;
+          rot_pair<true>(x[i], w.x, other[i], s, hi, odd);
+          x[i] = MODE == kRotOdd ? odd : hi;
+        }
+      }
     }
   }
 }
@@ -133,63 +178,79 @@ struct AppendArgs {
   __nv_bfloat16* hat[2];     // k, v
 };
 
-// One CTA a token: its cosines and sines once, then 16 heads at a time, each
-// by 16 lanes.
+// A CTA a token (and a share of its heads, where tokens are few): its cosines and
+// sines once, then two heads a warp, of one kind, 16 lanes each.  The first
+// heads' loads are under way while the angles are turned into cosines.
 template <class T, int RD>
 __global__ void __launch_bounds__(kAppThreads) kv4_append_kernel(const AppendArgs a) {
   __shared__ float2 cs[RD ? RD / 2 : 1];
   const int t = blockIdx.x;
+  const int n_kv = a.c.n_heads, kv2 = (n_kv + 1) / 2, q2 = (a.n_q + 1) / 2;
+  const int items = 2 * kv2 + q2, step = gridDim.y * (kAppThreads / 32);
+  const int l = threadIdx.x & 15, second = (threadIdx.x >> 4) & 1;
+  int item = blockIdx.y * (kAppThreads / 32) + (threadIdx.x >> 5);
+  // an item: kind 0 a pair of key heads, 1 of values, 2 of queries
+  const auto load = [&](int it, int& kind, int& h, bool& on, float(&x)[8]) {
+    kind = it < kv2 ? 0 : it < 2 * kv2 ? 1 : 2;
+    h = 2 * (kind == 0 ? it : kind == 1 ? it - kv2 : it - 2 * kv2) + second;
+    on = it < items && h < (kind == 2 ? a.n_q : n_kv);
+    if (on) {
+      const T* p = static_cast<const T*>(kind == 0 ? a.x[1] : kind == 1 ? a.x[2] : a.x[0]);
+      const int64_t stride = kind == 0 ? a.stride[1] : kind == 1 ? a.stride[2] : a.stride[0];
+      load8(p + t * stride + h * kKvDim + 8 * l, x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+  };
+  int kind, h;
+  bool on;
+  float x[8];
+  load(item, kind, h, on, x);
   const int row = __ldg(a.seq + t);
   const int64_t pos = __ldg(a.pos + t);
+  const int64_t angle_at = a.positions ? __ldg(a.positions + t) : pos;
   if (row < 0 || row >= a.c.B || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return;
   const int pg = (int)pos / a.c.page_size, slot = (int)pos - pg * a.c.page_size;
   const int page = __ldg(a.c.table + row * a.c.table_stride + pg);
+  if (RD && threadIdx.x < RD / 2) cs[threadIdx.x] = rope_cos_sin(angle_at, __ldg(a.inv_freq + threadIdx.x));
   if (page < 0 || page >= a.c.n_pages) return;
-  if (RD && threadIdx.x < RD / 2)
-    cs[threadIdx.x] = rope_cos_sin(a.positions ? __ldg(a.positions + t) : pos, __ldg(a.inv_freq + threadIdx.x));
   __syncthreads();
-  const int l = threadIdx.x & 15;
-  const int n_kv = a.c.n_heads, units = a.n_q + 2 * n_kv;
-  // a warp's two units run together (the shuffles need both halves): round up
-  for (int u0 = 0; u0 < units; u0 += kAppUnits) {
-    const int u = u0 + (threadIdx.x >> 4);
-    const bool on = u < units;
-    const int which = u < a.n_q ? 0 : u < a.n_q + n_kv ? 1 : 2;
-    const int h = which == 0 ? u : which == 1 ? u - a.n_q : u - a.n_q - n_kv;
-    float x[8] = {}, odd[8];
-    if (on) load8(static_cast<const T*>(a.x[which]) + t * a.stride[which] + h * kKvDim + 8 * l, x);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
-    rotate8<RD>(y, odd, l, cs);
-    if (which == 2) {  // values are stored as they are
-#pragma unroll
-      for (int i = 0; i < 8; ++i) odd[i] = x[i];
-    }
-    uint32_t byte, codes;
-    quant8(odd, byte, codes);
-    uint32_t b = byte << (8 * (l >> 2));  // the record's four scales, from lanes 0, 4, 8, 12
-    b |= __shfl_xor_sync(0xffffffffu, b, 4);
-    b |= __shfl_xor_sync(0xffffffffu, b, 8);
-    if (!on) continue;
-    if (which == 0) {
-      // fp32: the rounded sum; narrower types round once, from the odd one
-      T* o = static_cast<T*>(a.q_out) + t * a.q_out_stride + h * kKvDim + 8 * l;
-      if (sizeof(T) == 4) store8(o, y);
-      else store8(o, odd);
+  while (item < items) {
+    int kind_next, h_next;
+    bool on_next;
+    float x_next[8];
+    load(item + step, kind_next, h_next, on_next, x_next);
+    if (kind == 2) {
+      // fp32 rounds once; a 16-bit type from a value within 1.5 units of fp32
+      rotate8<RD, sizeof(T) == 4 ? kRotFull : kRotNear>(x, l, cs);
+      if (on) store8(static_cast<T*>(a.q_out) + t * a.q_out_stride + h * kKvDim + 8 * l, x);
     } else {
-      uint8_t* blk = (which == 1 ? a.c.k : a.c.v) + page * a.c.page_stride + h * a.c.head_stride;
-      *reinterpret_cast<uint32_t*>(blk + slot * kKvCodeBytes + 4 * l) = codes;
-      if (l == 0)
-        *reinterpret_cast<uint32_t*>(blk + a.c.page_size * kKvCodeBytes + slot * kKvScaleBytes) = b;
-      if (__nv_bfloat16* hat = a.hat[which - 1]) {
-        const float s = e8m0_value(byte);
-        float val[8];
+      if (kind == 0) rotate8<RD, kRotOdd>(x, l, cs);
+      uint32_t byte, codes;
+      quant8(x, byte, codes);
+      uint32_t b = byte << (8 * (l >> 2));  // the record's four scales, from lanes 0, 4, 8, 12
+      b |= __shfl_xor_sync(0xffffffffu, b, 4);
+      b |= __shfl_xor_sync(0xffffffffu, b, 8);
+      if (on) {
+        uint8_t* blk = (kind == 0 ? a.c.k : a.c.v) + page * a.c.page_stride + h * a.c.head_stride;
+        *reinterpret_cast<uint32_t*>(blk + slot * kKvCodeBytes + 4 * l) = codes;
+        if (l == 0) *reinterpret_cast<uint32_t*>(blk + a.c.page_size * kKvCodeBytes + slot * kKvScaleBytes) = b;
+        if (__nv_bfloat16* hat = kind == 0 ? a.hat[0] : a.hat[1]) {
+          const float s = e8m0_value(byte);
+          float val[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) val[i] = e2m1_value((codes >> (4 * i)) & 15u) * s;
-        store8(hat + ((int64_t)t * n_kv + h) * kKvDim + 8 * l, val);
+          for (int i = 0; i < 8; ++i) val[i] = e2m1_value((codes >> (4 * i)) & 15u) * s;
+          store8(hat + ((int64_t)t * n_kv + h) * kKvDim + 8 * l, val);
+        }
       }
     }
+    item += step;
+    kind = kind_next;
+    h = h_next;
+    on = on_next;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x_next[i];
   }
 }
 
@@ -216,26 +277,27 @@ __device__ __forceinline__ float e4m3_scale(float amax, float& inv) {
   return scale;
 }
 
-// 16 lanes a key, 16 keys a CTA.
+// 16 lanes a key, the keys of 16 / L tokens a CTA: a token's cosines and sines
+// serve all its layers.
 template <class T, int RD>
 __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexArgs a) {
   __shared__ float2 cs[kAppUnits][RD ? RD / 2 : 1];
-  const int64_t u = (int64_t)blockIdx.x * kAppUnits + (threadIdx.x >> 4);
+  const int per = kAppUnits / a.L;  // tokens a CTA
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const bool in = u < (int64_t)a.T * a.L;
-  const int t = in ? (int)(u / a.L) : 0, layer = in ? (int)(u - (int64_t)t * a.L) : 0;
+  const int tok = w / a.L, layer = w - tok * a.L, t = blockIdx.x * per + tok;
+  const bool in = tok < per && t < a.T;
   const int row = in ? __ldg(a.row + t) : -1, chunk = in ? __ldg(a.chunk + t) : -1;
   const bool on = row >= 0 && row < a.B && chunk >= 0 && chunk < a.N;
-  float x[8] = {}, odd[8];
-  if (on) {
-    load8(static_cast<const T*>(a.k) + t * a.stride + layer * kKvDim + 8 * l, x);
-    if (RD) {
-      const int64_t p = __ldg(a.positions + t);
-      for (int j = l; j < RD / 2; j += 16) cs[w][j] = rope_cos_sin(p, __ldg(a.inv_freq + j));
+  float x[8] = {};
+  if (in) load8(static_cast<const T*>(a.k) + t * a.stride + layer * kKvDim + 8 * l, x);
+  if (RD) {
+    for (int i = threadIdx.x; i < per * (RD / 2); i += kAppThreads) {
+      const int tt = blockIdx.x * per + i / (RD / 2);
+      if (tt < a.T) cs[i / (RD / 2)][i % (RD / 2)] = rope_cos_sin(__ldg(a.positions + tt), __ldg(a.inv_freq + i % (RD / 2)));
     }
+    __syncthreads();
   }
-  __syncwarp();
-  rotate8<RD>(x, odd, l, cs[w]);
+  rotate8<RD, kRotNear>(x, l, cs[tok < per ? tok : 0]);
   if (a.hadamard) {
 #pragma unroll
     for (int s = 1; s < 8; s <<= 1)
@@ -347,7 +409,10 @@ extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_de
   return by_dtype(d->dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
     return by_rope_dim(d->rope_dim, [&](auto rd) {
-      kv4_append_kernel<T, decltype(rd)::value><<<d->T, kAppThreads, 0, stream>>>(a);
+      // few tokens: their heads over as many CTAs as there are shares of 16 heads, up to four CTAs an SM
+      const int shares = (2 * ((c->n_kv_heads + 1) / 2) + (a.n_q + 1) / 2 + kAppThreads / 32 - 1) / (kAppThreads / 32);
+      const int y = std::max(1, std::min(shares, 4 * 148 / d->T));
+      kv4_append_kernel<T, decltype(rd)::value><<<dim3(d->T, y), kAppThreads, 0, stream>>>(a);
       note_launch();
       return check_launch();
     });
@@ -363,7 +428,6 @@ extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_str
   if (rope_dim != 0 && rope_dim != 64 && rope_dim != 128) return FM_ERR_UNSUPPORTED;
   if (rope_dim && (!positions || !inv_freq)) return FM_ERR_INVALID_ARG;
   if (token_stride < (int64_t)L * kKvDim || row_stride_bytes < (int64_t)N * kRecord) return FM_ERR_INVALID_ARG;
-  if ((int64_t)T * L > ((int64_t)1 << 34)) return FM_ERR_INVALID_ARG;
   if (!aligned16(k) || (token_stride * dtype_size(dtype)) % 16 || row_stride_bytes % 4 ||
       (reinterpret_cast<uintptr_t>(row) & 3u) || (reinterpret_cast<uintptr_t>(chunk) & 3u) ||
       (reinterpret_cast<uintptr_t>(positions) & 7u) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
@@ -383,7 +447,8 @@ extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_str
   a.row_stride = row_stride_bytes;
   a.T = T; a.L = L; a.B = B; a.N = N;
   a.hadamard = hadamard != 0;
-  const unsigned grid = (unsigned)(((int64_t)T * L + kAppUnits - 1) / kAppUnits);
+  const int per = kAppUnits / L;
+  const unsigned grid = (unsigned)(((int64_t)T + per - 1) / per);
   return by_dtype(dtype, [&](auto* tag) {
     using E = std::remove_pointer_t<decltype(tag)>;
     return by_rope_dim(rope_dim, [&](auto rd) {

@@ -573,52 +573,50 @@ def fm_select_topk_sharded(ens_local: torch.Tensor, k: int, n_valid_local: Optio
 # ------------------------------------------------- the 4-bit paged cache
 
 
-class _On:
-    """Where a call runs: the device its tensors are on, and the stream (the
-    device's current one unless the caller names another).  As a context it
-    makes that device the current one for the C call.  Memory that the call
-    allocates comes from the stream's own pool, and the tensors of a call on a
-    side stream are recorded there, so that none is handed out again while the
-    kernels still use it."""
+def _where(stream, first, *others):
+    """Where a call runs: the index of the device that all its tensors are on,
+    the raw stream (the device's current one unless the caller names another)
+    and, if that is another, the stream itself: the call's tensors are then
+    recorded on it, so that none is handed out again while its kernels use it."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"the tensors must be on one device, got {first.device} and {t.device}")
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or stream.cuda_stream == raw and stream.device_index == index:
+        return index, raw, None
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+    for t in (first, *others):
+        if t is not None:
+            t.record_stream(stream)
+    return index, stream.cuda_stream, stream
 
-    __slots__ = ("index", "stream", "side", "back")
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        if dev.type != "cuda":
-            raise ValueError("the tensors must be CUDA tensors")
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"the tensors must be on one device, got {dev} and {t.device}")
-        self.index, self.side, self.back = dev.index, None, -1
-        if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(dev.index)
-        else:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            self.stream = stream.cuda_stream
-            if self.stream != torch._C._cuda_getCurrentRawStream(dev.index):
-                self.side = stream
-                for t in tensors:
-                    if t is not None:
-                        t.record_stream(stream)
+def _new(make, like, shape, dtype, side):
+    """make = torch.empty or torch.zeros, on like's device; from the side
+    stream's own pool where the call runs on one (its memory may then be used
+    there at once) and recorded on the current stream, where the caller goes on."""
+    if side is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(side):
+        t = make(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
-    def new(self, make, shape, dtype):
-        """make = torch.empty or torch.zeros."""
-        dev = torch.device("cuda", self.index)
-        if self.side is None:
-            return make(shape, dtype=dtype, device=dev)
-        with torch.cuda.stream(self.side):
-            t = make(shape, dtype=dtype, device=dev)
-        t.record_stream(torch.cuda.current_stream(dev))
-        return t
 
-    def __enter__(self):
-        self.back = torch._C._cuda_exchangeDevice(self.index)
-        return self
-
-    def __exit__(self, *exc):
-        torch._C._cuda_exchangeDevice(self.back)
+def _run(index, name, fn, *args):
+    """The C call with its tensors' device as the current one."""
+    back = torch._C._cuda_exchangeDevice(index)
+    try:
+        status = fn(*args)
+    finally:
+        if back != index:
+            torch._C._cuda_exchangeDevice(back)
+    if status:
+        raise FMError(status, name)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -626,36 +624,40 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 def _like(t: torch.Tensor, shape, dtype, name: str):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _heads(t: torch.Tensor, T: int, name: str, dtype=None) -> int:
     """[T, heads, 128] with packed heads -> the stride between tokens, in elements."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != 128 or t.dtype not in DTYPES:
-        raise ValueError(f"{name} must be [{T}, heads, 128] fp32, bf16 or fp16, got {t.dtype} {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != 128 or t.dtype not in DTYPES:
+        raise ValueError(f"{name} must be [{T}, heads, 128] fp32, bf16 or fp16, got {t.dtype} {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128):
+    st = t.stride()
+    if st[2] != 1 or (st[1] != 128 and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be packed")
-    return t.stride(0) if T > 1 else t.shape[1] * 128
+    return st[0] if T > 1 else shape[1] * 128
 
 
 def _kv4_cache(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor) -> fm_kv4_cache:
-    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8 or k_pages.dim() != 3:
+    shape, st = k_pages.shape, k_pages.stride()
+    if k_pages.dtype != torch.uint8 or v_pages.dtype != torch.uint8 or len(shape) != 3:
         raise ValueError("the pages must be uint8 [n_pages, n_kv_heads, page_size * 68]")
-    n_pages, n_heads, block = k_pages.shape
-    if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+    n_pages, n_heads, block = shape
+    if v_pages.shape != shape or v_pages.stride() != st:
         raise ValueError("k_pages and v_pages must have the same shape and strides")
-    if block % FM_KV4_TOKEN_BYTES or k_pages.stride(2) != 1:
+    if block % FM_KV4_TOKEN_BYTES or st[2] != 1:
         raise ValueError("a page's block must be page_size * 68 contiguous bytes")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+    rows = page_table.stride()
+    if page_table.dtype != torch.int32 or len(rows) != 2 or (rows[1] != 1 and page_table.shape[1] > 1):
         raise ValueError("page_table must be int32 [B, max_pages] with contiguous rows")
     B, max_pages = page_table.shape
-    head = k_pages.stride(1) if n_heads > 1 else block
-    page = k_pages.stride(0) if n_pages > 1 else max(n_heads * head, block)
+    head = st[1] if n_heads > 1 else block
+    page = st[0] if n_pages > 1 else max(n_heads * head, block)
     return fm_kv4_cache(k_pages.data_ptr(), v_pages.data_ptr(), page, head, n_pages, block // FM_KV4_TOKEN_BYTES,
-                        n_heads, B, max_pages, page_table.stride(0) if B > 1 else max_pages, page_table.data_ptr())
+                        n_heads, B, max_pages, rows[0] if B > 1 else max_pages, page_table.data_ptr())
 
 
 def _check_freq(inv_freq: Optional[torch.Tensor]) -> int:
@@ -708,31 +710,32 @@ def fm_kv4_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pag
     if positions is not None:
         _like(positions, (T,), torch.int64, "positions")
     rope_dim = _check_freq(inv_freq)
-    on = _On(stream, k, v, k_pages, v_pages, page_table, seq, pos, inv_freq, positions, q, q_out, k_hat, v_hat)
+    index, raw, side = _where(stream, k, v, k_pages, v_pages, page_table, seq, pos, inv_freq, positions, q, q_out, k_hat,
+                              v_hat)
     n_q = qs = qos = 0
     if q is not None:
         n_q, qs = q.shape[1], _heads(q, T, "q", k.dtype)
         if q_out is None:
-            q_out = on.new(torch.zeros, (T, n_q, 128), k.dtype)
+            q_out = _new(torch.zeros, k, (T, n_q, 128), k.dtype, side)
         qos = _heads(q_out, T, "q_out", k.dtype)
         if q_out.shape[1] != n_q:
             raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out without q")
     if values and k_hat is None:
-        k_hat = on.new(torch.zeros, tuple(k.shape), torch.bfloat16)
+        k_hat = _new(torch.zeros, k, k.shape, torch.bfloat16, side)
     if values and v_hat is None:
-        v_hat = on.new(torch.zeros, tuple(k.shape), torch.bfloat16)
-    for t, name in ((k_hat, "k_hat"), (v_hat, "v_hat")):
-        if t is not None:
-            _like(t, k.shape, torch.bfloat16, name)
+        v_hat = _new(torch.zeros, k, k.shape, torch.bfloat16, side)
+    if k_hat is not None:
+        _like(k_hat, k.shape, torch.bfloat16, "k_hat")
+    if v_hat is not None:
+        _like(v_hat, k.shape, torch.bfloat16, "v_hat")
     if T == 0:
         return q_out, k_hat, v_hat
     d = fm_kv4_append_desc(DTYPES[k.dtype], T, n_q, k.data_ptr(), v.data_ptr(), _addr(q), ks, vs, qs, qos,
                            seq.data_ptr(), pos.data_ptr(), _addr(positions), _addr(inv_freq), rope_dim, _addr(q_out),
                            _addr(k_hat), _addr(v_hat))
-    with on:
-        _check(_lib.fm_kv4_append(ctypes.byref(cache), ctypes.byref(d), on.stream), "fm_kv4_append")
+    _run(index, "fm_kv4_append", _lib.fm_kv4_append, ctypes.byref(cache), ctypes.byref(d), raw)
     return q_out, k_hat, v_hat
 
 
@@ -752,18 +755,18 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     visible position), idx / count (fm_compact_mask's list: only the kept
     positions are read).  max_len bounds kv_len where the caller knows it.
     Returns the output in q's type and shape; 0 for a query that sees nothing."""
-    one = q.dim() == 3
-    if q.dim() not in (3, 4) or q.shape[-1] != 128 or q.dtype not in DTYPES:
+    shape, st = q.shape, q.stride()
+    if len(shape) not in (3, 4) or shape[-1] != 128 or q.dtype not in DTYPES:
         raise ValueError("q must be [B, heads, 128] or [B, Tq, heads, 128] fp32, bf16 or fp16")
-    B, Tq, n_q = q.shape[0], 1 if one else q.shape[1], q.shape[-2]
-    if q.stride(-1) != 1 or (n_q > 1 and q.stride(-2) != 128):
+    B, Tq, n_q = shape[0], 1 if len(shape) == 3 else shape[1], shape[-2]
+    if st[-1] != 1 or (n_q > 1 and st[-2] != 128):
         raise ValueError("the heads of a token of q must be packed")
     if Tq > 1:
-        qs = q.stride(1)
-        if B > 1 and q.stride(0) != Tq * qs:
+        qs = st[1]
+        if B > 1 and st[0] != Tq * qs:
             raise ValueError("the tokens of q must be evenly spaced")
     else:
-        qs = q.stride(0) if B > 1 else n_q * 128
+        qs = st[0] if B > 1 else n_q * 128
     cache = _kv4_cache(k_pages, v_pages, page_table)
     if page_table.shape[0] != B:
         raise ValueError("page_table must have a row for each of q's")
@@ -781,10 +784,12 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         _like(count, (B,), torch.int32, "count")
     elif count is not None:
         raise ValueError("count without idx")
-    on = _On(stream, q, k_pages, v_pages, page_table, kv_len, slopes, kv_start, idx, count, out, workspace)
+    index, raw, side = _where(stream, q, k_pages, v_pages, page_table, kv_len, slopes, kv_start, idx, count, out,
+                              workspace)
     if out is None:
-        out = on.new(torch.empty, tuple(q.shape), q.dtype)
-    _like(out, q.shape, q.dtype, "out")
+        out = _new(torch.empty, q, q.shape, q.dtype, side)
+    else:
+        _like(out, q.shape, q.dtype, "out")
     if out.numel() == 0:
         return out
     if idx is not None and max_sel == 0:
@@ -795,11 +800,10 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                          128 ** -0.5 if scale is None else float(scale), float(softcap), _addr(slopes), int(window))
     rc, rd = ctypes.byref(cache), ctypes.byref(d)
     if workspace is None:
-        workspace = on.new(torch.empty, (max(16, _lib.fm_kv4_attention_workspace_bytes(rc, rd)),), torch.uint8)
+        workspace = _new(torch.empty, q, max(16, _lib.fm_kv4_attention_workspace_bytes(rc, rd)), torch.uint8, side)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    with on:
-        _check(_lib.fm_kv4_attention(rc, rd, workspace.data_ptr(), workspace.numel(), on.stream), "fm_kv4_attention")
+    _run(index, "fm_kv4_attention", _lib.fm_kv4_attention, rc, rd, workspace.data_ptr(), workspace.numel(), raw)
     return out
 
 
@@ -829,14 +833,12 @@ def fm_index_append(k: torch.Tensor, comp_k: Sequence[torch.Tensor], row: torch.
     N = N_pad if N is None else int(N)
     if N > N_pad:
         raise ValueError("N exceeds the rows of comp_k")
-    on = _On(stream, k, *comp_k, row, chunk, inv_freq, positions)
+    index, raw, _ = _where(stream, k, *comp_k, row, chunk, inv_freq, positions)
     if T == 0 or N == 0 or B == 0:
         return
     arr = (ctypes.c_void_p * L)(*[t.data_ptr() for t in comp_k])
-    with on:
-        _check(_lib.fm_index_append(k.data_ptr(), DTYPES[k.dtype], ks, T, L, row.data_ptr(), chunk.data_ptr(),
-                                    _addr(positions), _addr(inv_freq), rope_dim, 1 if hadamard else 0, arr,
-                                    N_pad * 132, B, N, on.stream), "fm_index_append")
+    _run(index, "fm_index_append", _lib.fm_index_append, k.data_ptr(), DTYPES[k.dtype], ks, T, L, row.data_ptr(),
+         chunk.data_ptr(), _addr(positions), _addr(inv_freq), rope_dim, 1 if hadamard else 0, arr, N_pad * 132, B, N, raw)
 
 
 def fm_add_rmsnorm_fp8(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -857,23 +859,25 @@ def fm_add_rmsnorm_fp8(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
     group = int(group)
     if group < 1 or H % group:
         raise ValueError("group must be 128 or H")
-    on = _On(stream, x, residual, gain, sum_out, codes, scales)
+    index, raw, side = _where(stream, x, residual, gain, sum_out, codes, scales)
     if sum_out is None:
-        sum_out = on.new(torch.empty, (T, H), x.dtype)
+        sum_out = _new(torch.empty, x, (T, H), x.dtype, side)
+    else:
+        _like(sum_out, (T, H), x.dtype, "sum_out")
     if codes is None:
-        codes = on.new(torch.empty, (T, H), torch.float8_e4m3fn)
+        codes = _new(torch.empty, x, (T, H), torch.float8_e4m3fn, side)
+    else:
+        _like(codes, (T, H), codes.dtype if codes.dtype == torch.uint8 else torch.float8_e4m3fn, "codes")
     if scales is None:
-        scales = on.new(torch.empty, (T, H // group), torch.float32)
-    _like(sum_out, (T, H), x.dtype, "sum_out")
-    _like(codes, (T, H), codes.dtype if codes.dtype == torch.uint8 else torch.float8_e4m3fn, "codes")
-    _like(scales, (T, H // group), torch.float32, "scales")
+        scales = _new(torch.empty, x, (T, H // group), torch.float32, side)
+    else:
+        _like(scales, (T, H // group), torch.float32, "scales")
     if T == 0:
         return sum_out, codes, scales
     rs = 0 if residual is None else residual.stride(0) if T > 1 else H
-    with on:
-        _check(_lib.fm_add_rmsnorm_fp8(x.data_ptr(), x.stride(0) if T > 1 else H, _addr(residual), rs, _addr(gain),
-                                       DTYPES[x.dtype], T, H, float(eps), group, sum_out.data_ptr(), codes.data_ptr(),
-                                       scales.data_ptr(), on.stream), "fm_add_rmsnorm_fp8")
+    _run(index, "fm_add_rmsnorm_fp8", _lib.fm_add_rmsnorm_fp8, x.data_ptr(), x.stride(0) if T > 1 else H,
+         _addr(residual), rs, _addr(gain), DTYPES[x.dtype], T, H, float(eps), group, sum_out.data_ptr(),
+         codes.data_ptr(), scales.data_ptr(), raw)
     return sum_out, codes, scales
 
 

@@ -144,7 +144,7 @@ def test_bad_norms_are_refused():
 
     for kw, status in [(dict(x=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
                        (dict(dtype=4), INVALID), (dict(T=0), INVALID), (dict(H=0), INVALID), (dict(H=200), UNSUP),
-                       (dict(H=65664, xs=65664, rs=65664), UNSUP), (dict(group=64), UNSUP), (dict(eps=-1.0), INVALID),
+                       (dict(H=32896, xs=32896, rs=32896), UNSUP), (dict(group=64), UNSUP), (dict(eps=-1.0), INVALID),
                        (dict(eps=float("nan")), INVALID), (dict(xs=255), INVALID), (dict(rs=128), INVALID),
                        (dict(out=FAKE, xs=512), INVALID), (dict(out=FAKE + 65536, rs=512), INVALID),
                        (dict(x=FAKE + 4), ALIGN), (dict(r=FAKE + 4), ALIGN), (dict(gain=FAKE + 2), ALIGN),
