@@ -95,34 +95,55 @@ __device__ __forceinline__ float rot_near(float a, float c, float b, float s) {
   return __fadd_rn(__fmaf_rn(a, c, q), __fmaf_rn(bs, s, -q));
 }
 
-// Rotates the lane's 8 values of a head (lane l of 16 has dims 8l .. 8l+7).
-// cs: cos, sin of the token for j < RD / 2.  How a value comes back: ODD rounded to
-// odd (codes, and whatever else rounds it again), FULL rounded to fp32, NEAR
-// within 1.5 units of fp32.
+// A token's cosines and sines in shared memory: 8 pairs in every 10, so that the
+// lanes' 16-byte reads of 8 pairs each fall into different banks.
+constexpr int cs_place(int j) { return j / 8 * 10 + j % 8; }
+template <int RD>
+constexpr int kCsSize = RD ? RD / 16 * 10 : 2;
+
+// What lane l of 16 (dims 8l .. 8l+7) needs of them: a value becomes x cos - other
+// sin, with the sign of the second of a pair in the sine; 1 and 0 where nothing
+// turns.
+template <int RD>
+struct Turn {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const float2* cs, int l) {
+    if constexpr (RD != 0) {
+      constexpr int kHalfLanes = RD / 16, kFirst = (kKvDim - RD) / 8;
+      const bool in = l >= kFirst, second = l >= kFirst + kHalfLanes;
+      const float4* p = reinterpret_cast<const float4*>(cs + (in ? 10 * (second ? l - kFirst - kHalfLanes : l - kFirst) : 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 w = p[i];
+        c[2 * i] = in ? w.x : 1.f;
+        c[2 * i + 1] = in ? w.z : 1.f;
+        s[2 * i] = in ? (second ? -w.y : w.y) : 0.f;
+        s[2 * i + 1] = in ? (second ? -w.w : w.w) : 0.f;
+      }
+    }
+  }
+};
+
+// Rotates the lane's 8 values of a head.  How a value comes back: ODD rounded to
+// odd (for codes: whatever rounds it again), FULL rounded to fp32, NEAR within
+// 1.5 units of fp32.
 enum RotMode { kRotOdd, kRotFull, kRotNear };
 template <int RD, RotMode MODE>
-__device__ __forceinline__ void rotate8(float (&x)[8], int l, const float2* cs) {
+__device__ __forceinline__ void rotate8(float (&x)[8], int l, const Turn<RD>& w) {
   if constexpr (RD != 0) {
-    constexpr int kHalfLanes = RD / 16;              // lanes of half a pair range
-    constexpr int kFirst = (kKvDim - RD) / 8;        // first rotated lane
-    const bool in = l >= kFirst;
-    const bool second = in && l >= kFirst + kHalfLanes;
-    const int j0 = in ? 8 * (second ? l - kFirst - kHalfLanes : l - kFirst) : 0;
+    constexpr int kHalfLanes = RD / 16, kFirst = (kKvDim - RD) / 8;
     float other[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, x[i], kHalfLanes);
-    if (in) {
+    if (l < kFirst) return;  // a value with an infinity or a NaN opposite stays what it is
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 w = cs[j0 + i];
-        const float s = second ? -w.y : w.y;  // x1 c - x2 s, and x2 c - x1 (-s)
-        if (MODE == kRotNear) {
-          x[i] = rot_near<true>(x[i], w.x, other[i], s);
-        } else {
-          float hi, odd;
-          rot_pair<true>(x[i], w.x, other[i], s, hi, odd);
-          x[i] = MODE == kRotOdd ? odd : hi;
-        }
+    for (int i = 0; i < 8; ++i) {
+      if (MODE == kRotNear) {
+        x[i] = rot_near<true>(x[i], w.c[i], other[i], w.s[i]);
+      } else {
+        float hi, odd;
+        rot_pair<true>(x[i], w.c[i], other[i], w.s[i], hi, odd);
+        x[i] = MODE == kRotOdd ? odd : hi;
       }
     }
   }
@@ -157,11 +178,17 @@ __device__ __forceinline__ void quant8(const float (&x)[8], uint32_t& byte, uint
   codes = w & (0x77777777u | (nz << 3));
 }
 
-// The value of e2m1 code c (4 bits), fp32.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float v = e ? __uint_as_float(((e + 126u) << 23) | (m << 22)) : 0.5f * (float)m;
-  return (c & 8u) ? -v : v;
+// The values of 8 codes times a scale, as bf16 (exact), stored.
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t codes, float scale) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((codes >> (8 * i)) & 255u), __NV_E2M1);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 struct AppendArgs {
@@ -183,74 +210,61 @@ struct AppendArgs {
 // heads' loads are under way while the angles are turned into cosines.
 template <class T, int RD>
 __global__ void __launch_bounds__(kAppThreads) kv4_append_kernel(const AppendArgs a) {
-  __shared__ float2 cs[RD ? RD / 2 : 1];
+  __shared__ alignas(16) float2 cs[kCsSize<RD>];
   const int t = blockIdx.x;
   const int n_kv = a.c.n_heads, kv2 = (n_kv + 1) / 2, q2 = (a.n_q + 1) / 2;
   const int items = 2 * kv2 + q2, step = gridDim.y * (kAppThreads / 32);
   const int l = threadIdx.x & 15, second = (threadIdx.x >> 4) & 1;
-  int item = blockIdx.y * (kAppThreads / 32) + (threadIdx.x >> 5);
-  // an item: kind 0 a pair of key heads, 1 of values, 2 of queries
-  const auto load = [&](int it, int& kind, int& h, bool& on, float(&x)[8]) {
-    kind = it < kv2 ? 0 : it < 2 * kv2 ? 1 : 2;
-    h = 2 * (kind == 0 ? it : kind == 1 ? it - kv2 : it - 2 * kv2) + second;
-    on = it < items && h < (kind == 2 ? a.n_q : n_kv);
-    if (on) {
-      const T* p = static_cast<const T*>(kind == 0 ? a.x[1] : kind == 1 ? a.x[2] : a.x[0]);
-      const int64_t stride = kind == 0 ? a.stride[1] : kind == 1 ? a.stride[2] : a.stride[0];
-      load8(p + t * stride + h * kKvDim + 8 * l, x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
+  // an item is a pair of heads: kind 0 of keys, 1 of values, 2 of queries; a lane's eight dims of one of them
+  const auto kind_of = [&](int it) { return it < kv2 ? 0 : it < 2 * kv2 ? 1 : 2; };
+  const auto head_of = [&](int it, int kind) { return 2 * (it - kind * kv2) + second; };
+  const T* src[3] = {static_cast<const T*>(a.x[1]) + t * a.stride[1], static_cast<const T*>(a.x[2]) + t * a.stride[2],
+                     static_cast<const T*>(a.x[0]) + t * a.stride[0]};
+  const auto load = [&](int it) {
+    const int kind = kind_of(it), h = head_of(it, kind);
+    Raw8<T> r = {};
+    if (it < items && h < (kind == 2 ? a.n_q : n_kv))
+      r = load_raw8((kind == 0 ? src[0] : kind == 1 ? src[1] : src[2]) + h * kKvDim + 8 * l);
+    return r;
   };
-  int kind, h;
-  bool on;
-  float x[8];
-  load(item, kind, h, on, x);
+  int item = blockIdx.y * (kAppThreads / 32) + (threadIdx.x >> 5);
+  Raw8<T> ahead[2] = {load(item), load(item + step)};
   const int row = __ldg(a.seq + t);
   const int64_t pos = __ldg(a.pos + t);
   const int64_t angle_at = a.positions ? __ldg(a.positions + t) : pos;
   if (row < 0 || row >= a.c.B || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return;
   const int pg = (int)pos / a.c.page_size, slot = (int)pos - pg * a.c.page_size;
   const int page = __ldg(a.c.table + row * a.c.table_stride + pg);
-  if (RD && threadIdx.x < RD / 2) cs[threadIdx.x] = rope_cos_sin(angle_at, __ldg(a.inv_freq + threadIdx.x));
+  if (RD && threadIdx.x < RD / 2) cs[cs_place(threadIdx.x)] = rope_cos_sin(angle_at, __ldg(a.inv_freq + threadIdx.x));
   if (page < 0 || page >= a.c.n_pages) return;
   __syncthreads();
-  while (item < items) {
-    int kind_next, h_next;
-    bool on_next;
-    float x_next[8];
-    load(item + step, kind_next, h_next, on_next, x_next);
+  Turn<RD> turn;
+  turn.load(cs, l);
+  for (; item < items; item += step) {
+    float x[8];
+    to_f32(ahead[0], x);
+    ahead[0] = ahead[1];
+    ahead[1] = load(item + 2 * step);
+    const int kind = kind_of(item), h = head_of(item, kind);
+    const bool on = h < (kind == 2 ? a.n_q : n_kv);
     if (kind == 2) {
       // fp32 rounds once; a 16-bit type from a value within 1.5 units of fp32
-      rotate8<RD, sizeof(T) == 4 ? kRotFull : kRotNear>(x, l, cs);
+      rotate8<RD, sizeof(T) == 4 ? kRotFull : kRotNear>(x, l, turn);
       if (on) store8(static_cast<T*>(a.q_out) + t * a.q_out_stride + h * kKvDim + 8 * l, x);
-    } else {
-      if (kind == 0) rotate8<RD, kRotOdd>(x, l, cs);
-      uint32_t byte, codes;
-      quant8(x, byte, codes);
-      uint32_t b = byte << (8 * (l >> 2));  // the record's four scales, from lanes 0, 4, 8, 12
-      b |= __shfl_xor_sync(0xffffffffu, b, 4);
-      b |= __shfl_xor_sync(0xffffffffu, b, 8);
-      if (on) {
-        uint8_t* blk = (kind == 0 ? a.c.k : a.c.v) + page * a.c.page_stride + h * a.c.head_stride;
-        *reinterpret_cast<uint32_t*>(blk + slot * kKvCodeBytes + 4 * l) = codes;
-        if (l == 0) *reinterpret_cast<uint32_t*>(blk + a.c.page_size * kKvCodeBytes + slot * kKvScaleBytes) = b;
-        if (__nv_bfloat16* hat = kind == 0 ? a.hat[0] : a.hat[1]) {
-          const float s = e8m0_value(byte);
-          float val[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) val[i] = e2m1_value((codes >> (4 * i)) & 15u) * s;
-          store8(hat + ((int64_t)t * n_kv + h) * kKvDim + 8 * l, val);
-        }
-      }
+      continue;
     }
-    item += step;
-    kind = kind_next;
-    h = h_next;
-    on = on_next;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x_next[i];
+    if (kind == 0) rotate8<RD, kRotOdd>(x, l, turn);
+    uint32_t byte, codes;
+    quant8(x, byte, codes);
+    uint32_t b = byte << (8 * (l >> 2));  // the record's four scales, from lanes 0, 4, 8, 12
+    b |= __shfl_xor_sync(0xffffffffu, b, 4);
+    b |= __shfl_xor_sync(0xffffffffu, b, 8);
+    if (!on) continue;
+    uint8_t* blk = (kind == 0 ? a.c.k : a.c.v) + page * a.c.page_stride + h * a.c.head_stride;
+    *reinterpret_cast<uint32_t*>(blk + slot * kKvCodeBytes + 4 * l) = codes;
+    if (l == 0) *reinterpret_cast<uint32_t*>(blk + a.c.page_size * kKvCodeBytes + slot * kKvScaleBytes) = b;
+    if (__nv_bfloat16* hat = kind == 0 ? a.hat[0] : a.hat[1])
+      store_values(hat + ((int64_t)t * n_kv + h) * kKvDim + 8 * l, codes, e8m0_value(byte));
   }
 }
 
@@ -281,7 +295,7 @@ __device__ __forceinline__ float e4m3_scale(float amax, float& inv) {
 // serve all its layers.
 template <class T, int RD>
 __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexArgs a) {
-  __shared__ float2 cs[kAppUnits][RD ? RD / 2 : 1];
+  __shared__ alignas(16) float2 cs[kAppUnits][kCsSize<RD>];
   const int per = kAppUnits / a.L;  // tokens a CTA
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int tok = w / a.L, layer = w - tok * a.L, t = blockIdx.x * per + tok;
@@ -293,11 +307,14 @@ __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexAr
   if (RD) {
     for (int i = threadIdx.x; i < per * (RD / 2); i += kAppThreads) {
       const int tt = blockIdx.x * per + i / (RD / 2);
-      if (tt < a.T) cs[i / (RD / 2)][i % (RD / 2)] = rope_cos_sin(__ldg(a.positions + tt), __ldg(a.inv_freq + i % (RD / 2)));
+      if (tt < a.T) cs[i / (RD / 2)][cs_place(i % (RD / 2))] =
+            rope_cos_sin(__ldg(a.positions + tt), __ldg(a.inv_freq + i % (RD / 2)));
     }
     __syncthreads();
   }
-  rotate8<RD, kRotNear>(x, l, cs[tok < per ? tok : 0]);
+  Turn<RD> turn;
+  turn.load(cs[tok < per ? tok : 0], l);
+  rotate8<RD, kRotNear>(x, l, turn);
   if (a.hadamard) {
 #pragma unroll
     for (int s = 1; s < 8; s <<= 1)
@@ -313,7 +330,7 @@ __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexAr
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float o = __shfl_xor_sync(0xffffffffu, x[i], s);
-        x[i] = (l & s) ? o - x[i] : x[i] + o;
+        x[i] = fmaf(x[i], (l & s) ? -1.f : 1.f, o);  // o + x, or o - x on the pair's second lane
       }
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] *= 0.08838834764831845f;  // 128^-1/2
@@ -333,7 +350,9 @@ __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexAr
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
     c[i] = lo | (hi << 16);
   }
-  uint32_t* rec = reinterpret_cast<uint32_t*>(a.comp_k[layer] + row * a.row_stride + (int64_t)chunk * kRecord);
+  // (chosen with constant indices: an index at run time would copy the array into local memory)
+  uint8_t* keys = layer == 0 ? a.comp_k[0] : layer == 1 ? a.comp_k[1] : layer == 2 ? a.comp_k[2] : a.comp_k[3];
+  uint32_t* rec = reinterpret_cast<uint32_t*>(keys + row * a.row_stride + (int64_t)chunk * kRecord);
   rec[2 * l] = c[0];
   rec[2 * l + 1] = c[1];
   if (l == 0) rec[32] = __float_as_uint(scale);
