@@ -584,7 +584,8 @@ fm_status fm_kv4_attention(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d,
  *   x = k[t, l] (rotated as in fm_kv4_append if rope_dim > 0), then, with
  *   hadamard, the normalised 128-point Walsh-Hadamard transform (the query's
  *   last step; a rotation of both sides leaves their products as they are);
- *   scale = max|x| / 448 in fp32, codes = e4m3(x * (1 / scale)), nearest even
+ *   scale = max|x| / 448 in fp32, codes = e4m3(x / scale), nearest even (formed
+ *   as x * (448 / max|x|))
  * into record chunk[t] of row row[t] of comp_k[l].  A key whose scale would be
  * below 2^-126 is stored as zeros with scale 0; one with a NaN or an infinity
  * gets a NaN scale.  A token with row[t] outside [0, B) or chunk[t] outside

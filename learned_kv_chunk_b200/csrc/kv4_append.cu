@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kAppThreads = 256;              // 16 heads of 16 lanes each
 constexpr int kAppUnits = kAppThreads / 16;
+constexpr int kAppWarps = kAppThreads / 32;
 
 // cos and sin of the fp64 angle position * f, rounded to fp32 once, as query prep
 // does.  The angle less the nearest multiple n of pi/2 (two fused steps with pi/2
@@ -199,47 +200,57 @@ struct AppendArgs {
   const int64_t* pos;
   const int64_t* positions;
   const double* inv_freq;
-  int n_q;
+  int n_q, T, wpt;
   void* q_out;
   int64_t q_out_stride;
   __nv_bfloat16* hat[2];     // k, v
 };
 
-// A CTA a token (and a share of its heads, where tokens are few): its cosines and
-// sines once, then two heads a warp, of one kind, 16 lanes each.  The first
-// heads' loads are under way while the angles are turned into cosines.
+// `wpt` warps a token (8 / wpt tokens a CTA), or a CTA and a share of its heads
+// where tokens are few: the token's cosines and sines once, then two heads a
+// warp, of one kind, 16 lanes each.  The first heads' loads are under way while
+// the angles are turned into cosines.
 template <class T, int RD>
 __global__ void __launch_bounds__(kAppThreads) kv4_append_kernel(const AppendArgs a) {
-  __shared__ alignas(16) float2 cs[kCsSize<RD>];
-  const int t = blockIdx.x;
+  __shared__ alignas(16) float2 cs[kAppWarps][kCsSize<RD>];
+  const int warp = threadIdx.x >> 5, l = threadIdx.x & 15, second = (threadIdx.x >> 4) & 1;
+  const int tpc = kAppWarps / a.wpt, local = warp / a.wpt, t = blockIdx.x * tpc + local;
+  const bool in = t < a.T;
   const int n_kv = a.c.n_heads, kv2 = (n_kv + 1) / 2, q2 = (a.n_q + 1) / 2;
-  const int items = 2 * kv2 + q2, step = gridDim.y * (kAppThreads / 32);
-  const int l = threadIdx.x & 15, second = (threadIdx.x >> 4) & 1;
+  const int items = 2 * kv2 + q2, step = gridDim.y * a.wpt;
   // an item is a pair of heads: kind 0 of keys, 1 of values, 2 of queries; a lane's eight dims of one of them
   const auto kind_of = [&](int it) { return it < kv2 ? 0 : it < 2 * kv2 ? 1 : 2; };
   const auto head_of = [&](int it, int kind) { return 2 * (it - kind * kv2) + second; };
-  const T* src[3] = {static_cast<const T*>(a.x[1]) + t * a.stride[1], static_cast<const T*>(a.x[2]) + t * a.stride[2],
-                     static_cast<const T*>(a.x[0]) + t * a.stride[0]};
+  const T* src[3] = {static_cast<const T*>(a.x[1]) + t * a.stride[1] + 8 * l, static_cast<const T*>(a.x[2]) + t * a.stride[2] + 8 * l,
+                     static_cast<const T*>(a.x[0]) + t * a.stride[0] + 8 * l};
   const auto load = [&](int it) {
     const int kind = kind_of(it), h = head_of(it, kind);
     Raw8<T> r = {};
-    if (it < items && h < (kind == 2 ? a.n_q : n_kv))
-      r = load_raw8((kind == 0 ? src[0] : kind == 1 ? src[1] : src[2]) + h * kKvDim + 8 * l);
+    if (in && it < items && h < (kind == 2 ? a.n_q : n_kv))
+      r = load_raw8((kind == 0 ? src[0] : kind == 1 ? src[1] : src[2]) + h * kKvDim);
     return r;
   };
-  int item = blockIdx.y * (kAppThreads / 32) + (threadIdx.x >> 5);
+  int item = blockIdx.y * a.wpt + warp - local * a.wpt;
   Raw8<T> ahead[2] = {load(item), load(item + step)};
-  const int row = __ldg(a.seq + t);
-  const int64_t pos = __ldg(a.pos + t);
-  const int64_t angle_at = a.positions ? __ldg(a.positions + t) : pos;
-  if (row < 0 || row >= a.c.B || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return;
-  const int pg = (int)pos / a.c.page_size, slot = (int)pos - pg * a.c.page_size;
-  const int page = __ldg(a.c.table + row * a.c.table_stride + pg);
-  if (RD && threadIdx.x < RD / 2) cs[cs_place(threadIdx.x)] = rope_cos_sin(angle_at, __ldg(a.inv_freq + threadIdx.x));
-  if (page < 0 || page >= a.c.n_pages) return;
+  const int row = in ? __ldg(a.seq + t) : -1;
+  const int64_t pos = in ? __ldg(a.pos + t) : -1;
+  if (RD) {
+    for (int i = threadIdx.x; i < tpc * (RD / 2); i += kAppThreads) {
+      const int tt = blockIdx.x * tpc + i / (RD / 2), j = i % (RD / 2);
+      if (tt < a.T)
+        cs[i / (RD / 2)][cs_place(j)] = rope_cos_sin(__ldg((a.positions ? a.positions : a.pos) + tt), __ldg(a.inv_freq + j));
+    }
+  }
+  int page = -1, slot = 0;
+  if (row >= 0 && row < a.c.B && pos >= 0 && pos < (int64_t)a.c.max_pages * a.c.page_size) {
+    const int pg = (int)pos / a.c.page_size;
+    slot = (int)pos - pg * a.c.page_size;
+    page = __ldg(a.c.table + row * a.c.table_stride + pg);
+  }
   __syncthreads();
+  if (page < 0 || page >= a.c.n_pages) return;  // padding
   Turn<RD> turn;
-  turn.load(cs, l);
+  turn.load(cs[local], l);
   for (; item < items; item += step) {
     float x[8];
     to_f32(ahead[0], x);
@@ -277,85 +288,85 @@ struct IndexArgs {
   const double* inv_freq;
   uint8_t* comp_k[kMaxLayers];
   int64_t row_stride;
-  int T, L, B, N, hadamard;
+  int T, L, B, N, hadamard, spread;
 };
 
 constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
 
-// The e4m3 codes of a lane's values over the scale of their amax.
-__device__ __forceinline__ float e4m3_scale(float amax, float& inv) {
-  float scale = amax / 448.f;
-  inv = scale >= kMinNormal ? 1.f / scale : 0.f;
-  if (scale < kMinNormal) scale = 0.f;
-  if (!(scale < INFINITY)) scale = nan_f32();
-  return scale;
-}
-
-// 16 lanes a key, the keys of 16 / L tokens a CTA: a token's cosines and sines
-// serve all its layers.
+// 16 lanes a key.  `spread` half-warps share a token's layers (all of them where
+// tokens are few, otherwise one: a token's setup then serves all its layers).
 template <class T, int RD>
 __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexArgs a) {
   __shared__ alignas(16) float2 cs[kAppUnits][kCsSize<RD>];
-  const int per = kAppUnits / a.L;  // tokens a CTA
+  const int per = kAppUnits / a.spread;  // tokens a CTA
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int tok = w / a.L, layer = w - tok * a.L, t = blockIdx.x * per + tok;
+  const int tok = w / a.spread, t = blockIdx.x * per + tok;
   const bool in = tok < per && t < a.T;
+  int layer = w - tok * a.spread;
+  const T* src = static_cast<const T*>(a.k) + t * a.stride + 8 * l;
+  Raw8<T> ahead = {};
+  if (in) ahead = load_raw8(src + layer * kKvDim);
   const int row = in ? __ldg(a.row + t) : -1, chunk = in ? __ldg(a.chunk + t) : -1;
   const bool on = row >= 0 && row < a.B && chunk >= 0 && chunk < a.N;
-  float x[8] = {};
-  if (in) load8(static_cast<const T*>(a.k) + t * a.stride + layer * kKvDim + 8 * l, x);
   if (RD) {
     for (int i = threadIdx.x; i < per * (RD / 2); i += kAppThreads) {
-      const int tt = blockIdx.x * per + i / (RD / 2);
-      if (tt < a.T) cs[i / (RD / 2)][cs_place(i % (RD / 2))] =
-            rope_cos_sin(__ldg(a.positions + tt), __ldg(a.inv_freq + i % (RD / 2)));
+      const int tt = blockIdx.x * per + i / (RD / 2), j = i % (RD / 2);
+      if (tt < a.T) cs[i / (RD / 2)][cs_place(j)] = rope_cos_sin(__ldg(a.positions + tt), __ldg(a.inv_freq + j));
     }
     __syncthreads();
   }
   Turn<RD> turn;
   turn.load(cs[tok < per ? tok : 0], l);
-  rotate8<RD, kRotNear>(x, l, turn);
-  if (a.hadamard) {
+  const int64_t at = on ? row * a.row_stride + (int64_t)chunk * kRecord : 0;
+  // (a warp's two tokens go through the same number of layers)
+  for (int i = 0; i < a.L; i += a.spread, layer += a.spread) {
+    float x[8];
+    to_f32(ahead, x);
+    if (in && layer + a.spread < a.L) ahead = load_raw8(src + (layer + a.spread) * kKvDim);
+    rotate8<RD, kRotNear>(x, l, turn);
+    if (a.hadamard) {
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1)
+      for (int s = 1; s < 8; s <<= 1)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (!(i & s)) {
-          const float p = x[i], q = x[i + s];
-          x[i] = p + q;
-          x[i + s] = p - q;
-        }
+        for (int i = 0; i < 8; ++i)
+          if (!(i & s)) {
+            const float p = x[i], q = x[i + s];
+            x[i] = p + q;
+            x[i + s] = p - q;
+          }
 #pragma unroll
-    for (int s = 1; s < 16; s <<= 1)
+      for (int s = 1; s < 16; s <<= 1) {
+        const float sign = (l & s) ? -1.f : 1.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_xor_sync(0xffffffffu, x[i], s);
-        x[i] = fmaf(x[i], (l & s) ? -1.f : 1.f, o);  // o + x, or o - x on the pair's second lane
+        for (int i = 0; i < 8; ++i)  // o + x, or o - x on the pair's second lane
+          x[i] = fmaf(x[i], sign, __shfl_xor_sync(0xffffffffu, x[i], s));
       }
+    }
+    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= 0.08838834764831845f;  // 128^-1/2
+    for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(x[i]));
+#pragma unroll
+    for (int s = 1; s < 16; s <<= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
+    if (!on || layer >= a.L) continue;
+    // the transform's 128^-1/2 joins the scale
+    float scale = m * (a.hadamard ? 0.08838834764831845f / 448.f : 1.f / 448.f);
+    float inv = 448.f / m;
+    if (scale < kMinNormal) scale = inv = 0.f;
+    if (!(scale < INFINITY)) scale = nan_f32();
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+      c[i] = lo | (hi << 16);
+    }
+    // (chosen with constant indices: an index at run time would copy the array into local memory)
+    uint8_t* keys = layer == 0 ? a.comp_k[0] : layer == 1 ? a.comp_k[1] : layer == 2 ? a.comp_k[2] : a.comp_k[3];
+    uint32_t* rec = reinterpret_cast<uint32_t*>(keys + at);
+    rec[2 * l] = c[0];
+    rec[2 * l + 1] = c[1];
+    if (l == 0) rec[32] = __float_as_uint(scale);
   }
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(x[i]));
-#pragma unroll
-  for (int s = 1; s < 16; s <<= 1) m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
-  if (!on) return;
-  float inv;
-  const float scale = e4m3_scale(m, inv);
-  uint32_t c[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-    c[i] = lo | (hi << 16);
-  }
-  // (chosen with constant indices: an index at run time would copy the array into local memory)
-  uint8_t* keys = layer == 0 ? a.comp_k[0] : layer == 1 ? a.comp_k[1] : layer == 2 ? a.comp_k[2] : a.comp_k[3];
-  uint32_t* rec = reinterpret_cast<uint32_t*>(keys + row * a.row_stride + (int64_t)chunk * kRecord);
-  rec[2 * l] = c[0];
-  rec[2 * l + 1] = c[1];
-  if (l == 0) rec[32] = __float_as_uint(scale);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -421,6 +432,7 @@ extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_de
   a.positions = d->positions;
   a.inv_freq = d->inv_freq;
   a.n_q = d->q ? d->n_q_heads : 0;
+  a.T = d->T;
   a.q_out = d->q_out;
   a.q_out_stride = d->q_out_stride;
   a.hat[0] = static_cast<__nv_bfloat16*>(d->k_hat);
@@ -428,10 +440,16 @@ extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_de
   return by_dtype(d->dtype, [&](auto* tag) {
     using T = std::remove_pointer_t<decltype(tag)>;
     return by_rope_dim(d->rope_dim, [&](auto rd) {
-      // few tokens: their heads over as many CTAs as there are shares of 16 heads, up to four CTAs an SM
-      const int shares = (2 * ((c->n_kv_heads + 1) / 2) + (a.n_q + 1) / 2 + kAppThreads / 32 - 1) / (kAppThreads / 32);
-      const int y = std::max(1, std::min(shares, 4 * 148 / d->T));
-      kv4_append_kernel<T, decltype(rd)::value><<<dim3(d->T, y), kAppThreads, 0, stream>>>(a);
+      // Warps a token: as few as leave two CTAs an SM (a token's setup is then shared by more heads: 8192 tokens of
+      // 48 heads take APPEND_8 us with eight warps each, APPEND_2 with two), eight where tokens are few, and then its
+      // heads over as many CTAs as there are shares of 16, up to four CTAs an SM (64 tokens of 80 heads: 12.5 us in
+      // one CTA a token, 4.3 in five).
+      const int items = 2 * ((c->n_kv_heads + 1) / 2) + (a.n_q + 1) / 2;
+      a.wpt = 2;
+      while (a.wpt < kAppWarps && (int64_t)d->T * a.wpt < 2 * 148 * kAppWarps) a.wpt *= 2;
+      const int y = a.wpt < kAppWarps ? 1 : std::max(1, std::min((items + kAppWarps - 1) / kAppWarps, 4 * 148 / d->T));
+      const int tpc = kAppWarps / a.wpt;
+      kv4_append_kernel<T, decltype(rd)::value><<<dim3((d->T + tpc - 1) / tpc, y), kAppThreads, 0, stream>>>(a);
       note_launch();
       return check_launch();
     });
@@ -466,7 +484,10 @@ extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_str
   a.row_stride = row_stride_bytes;
   a.T = T; a.L = L; a.B = B; a.N = N;
   a.hadamard = hadamard != 0;
-  const int per = kAppUnits / L;
+  // two CTAs an SM and more with a token a half-warp: 32768 tokens of three layers take INDEX_1 us (INDEX_L with a
+  // half-warp a key); fewer tokens spread their layers
+  a.spread = (int64_t)T >= 2 * 148 * kAppUnits ? 1 : L;
+  const int per = kAppUnits / a.spread;
   const unsigned grid = (unsigned)(((int64_t)T + per - 1) / per);
   return by_dtype(dtype, [&](auto* tag) {
     using E = std::remove_pointer_t<decltype(tag)>;
