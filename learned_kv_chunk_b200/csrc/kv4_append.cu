@@ -65,35 +65,47 @@ __device__ __forceinline__ float2 rope_cos_sin(int64_t position, double f) {
   return make_float2((float)c, (float)s);
 }
 
-// a * c - b * s (NEG) or a * c + b * s as the rounded sum `hi`, and the sum
-// rounded to odd.
-template <bool NEG>
-__device__ __forceinline__ void rot_pair(float a, float c, float b, float s, float& hi, float& odd) {
-  const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
-  const float bs = NEG ? -b : b;
-  const float q = __fmul_rn(bs, s), qe = __fmaf_rn(bs, s, -q);
-  // p + q as a pair, then the products' rests
-  const float t = __fadd_rn(p, q);
-  const float z = __fsub_rn(t, p);
-  const float te = __fadd_rn(__fsub_rn(p, __fsub_rn(t, z)), __fsub_rn(q, z));
-  const float lo0 = __fadd_rn(te, __fadd_rn(pe, qe));
-  hi = __fadd_rn(t, lo0);
-  const float lo = __fsub_rn(lo0, __fsub_rn(hi, t));
-  odd = hi;
-  if (lo != 0.f && isfinite(hi)) {
-    uint32_t u = __float_as_uint(hi);
-    if ((lo < 0.f) != (hi < 0.f)) u -= 1;  // the exact value is nearer to zero: truncate
-    odd = __uint_as_float(u | 1u);
-  }
+// Two fp32 values at a time (packed arithmetic halves the instructions, which
+// bound the appends).
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+constexpr uint64_t kMinusOnes = 0xbf800000bf800000ull;
+// a - b: one rounding, of the difference.
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, kMinusOnes, a); }
+
+// x c + o n as the rounded sum `hi` and what it leaves, `lo`: the products and
+// their rests, added as a pair.
+__device__ __forceinline__ void rot_pair(uint64_t x, uint64_t c, uint64_t o, uint64_t n, uint64_t& hi, uint64_t& lo) {
+  const uint64_t p = f2_mul(x, c), q = f2_mul(o, n);
+  const uint64_t pe = f2_fma(x, c, f2_mul(p, kMinusOnes)), qe = f2_fma(o, n, f2_mul(q, kMinusOnes));
+  const uint64_t t = f2_add(p, q), z = f2_sub(t, p);
+  const uint64_t te = f2_add(f2_sub(p, f2_sub(t, z)), f2_sub(q, z));
+  const uint64_t rest = f2_add(te, f2_add(pe, qe));
+  hi = f2_add(t, rest);
+  lo = f2_sub(rest, f2_sub(hi, t));
 }
 
-// a * c - b * s (NEG) or a * c + b * s within 1.5 units of fp32's last place,
-// whatever cancels: the second product's rounding is taken back.
-template <bool NEG>
-__device__ __forceinline__ float rot_near(float a, float c, float b, float s) {
-  const float bs = NEG ? -b : b;
-  const float q = __fmul_rn(bs, s);
-  return __fadd_rn(__fmaf_rn(a, c, q), __fmaf_rn(bs, s, -q));
+// hi + lo rounded to odd: truncated, with the last bit set if anything was cut.
+__device__ __forceinline__ float round_odd(float hi, float lo) {
+  const int u = __float_as_int(hi);
+  // of opposite signs: the exact value lies nearer to zero than hi
+  const int odd = (u + ((u ^ __float_as_int(lo)) >> 31)) | 1;
+  return fabsf(lo) > 0.f ? __int_as_float(odd) : hi;  // (an infinite or NaN hi has a NaN lo)
+}
+
+// x c + o n within 1.5 units of fp32's last place, whatever cancels: the second
+// product's rounding is taken back.
+__device__ __forceinline__ uint64_t rot_near(uint64_t x, uint64_t c, uint64_t o, uint64_t n) {
+  const uint64_t q = f2_mul(o, n);
+  return f2_add(f2_fma(x, c, q), f2_fma(o, n, f2_mul(q, kMinusOnes)));
 }
 
 // A token's cosines and sines in shared memory: 8 pairs in every 10, so that the
@@ -102,12 +114,11 @@ constexpr int cs_place(int j) { return j / 8 * 10 + j % 8; }
 template <int RD>
 constexpr int kCsSize = RD ? RD / 16 * 10 : 2;
 
-// What lane l of 16 (dims 8l .. 8l+7) needs of them: a value becomes x cos - other
-// sin, with the sign of the second of a pair in the sine; 1 and 0 where nothing
-// turns.
+// What lane l of 16 (dims 8l .. 8l+7) needs of them: a value becomes x c + other n,
+// n the sine or its negative; in pairs of dims.
 template <int RD>
 struct Turn {
-  float c[8], s[8];
+  uint64_t c[RD ? 4 : 1], n[RD ? 4 : 1];
   __device__ __forceinline__ void load(const float2* cs, int l) {
     if constexpr (RD != 0) {
       constexpr int kHalfLanes = RD / 16, kFirst = (kKvDim - RD) / 8;
@@ -116,10 +127,8 @@ struct Turn {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 w = p[i];
-        c[2 * i] = in ? w.x : 1.f;
-        c[2 * i + 1] = in ? w.z : 1.f;
-        s[2 * i] = in ? (second ? -w.y : w.y) : 0.f;
-        s[2 * i + 1] = in ? (second ? -w.w : w.w) : 0.f;
+        c[i] = f2_pack(w.x, w.z);
+        n[i] = second ? f2_pack(w.y, w.w) : f2_pack(-w.y, -w.w);
       }
     }
   }
@@ -136,15 +145,22 @@ __device__ __forceinline__ void rotate8(float (&x)[8], int l, const Turn<RD>& w)
     float other[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, x[i], kHalfLanes);
-    if (l < kFirst) return;  // a value with an infinity or a NaN opposite stays what it is
+    if (l < kFirst) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t a = f2_pack(x[2 * i], x[2 * i + 1]), b = f2_pack(other[2 * i], other[2 * i + 1]);
       if (MODE == kRotNear) {
-        x[i] = rot_near<true>(x[i], w.c[i], other[i], w.s[i]);
+        f2_unpack(rot_near(a, w.c[i], b, w.n[i]), x[2 * i], x[2 * i + 1]);
       } else {
-        float hi, odd;
-        rot_pair<true>(x[i], w.c[i], other[i], w.s[i], hi, odd);
-        x[i] = MODE == kRotOdd ? odd : hi;
+        uint64_t hi, lo;
+        rot_pair(a, w.c[i], b, w.n[i], hi, lo);
+        f2_unpack(hi, x[2 * i], x[2 * i + 1]);
+        if (MODE == kRotOdd) {
+          float l0, l1;
+          f2_unpack(lo, l0, l1);
+          x[2 * i] = round_odd(x[2 * i], l0);
+          x[2 * i + 1] = round_odd(x[2 * i + 1], l1);
+        }
       }
     }
   }
@@ -211,7 +227,7 @@ struct AppendArgs {
 // warp, of one kind, 16 lanes each.  The first heads' loads are under way while
 // the angles are turned into cosines.
 template <class T, int RD>
-__global__ void __launch_bounds__(kAppThreads) kv4_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppThreads, sizeof(T) == 2 ? 4 : 3) kv4_append_kernel(const AppendArgs a) {
   __shared__ alignas(16) float2 cs[kAppWarps][kCsSize<RD>];
   const int warp = threadIdx.x >> 5, l = threadIdx.x & 15, second = (threadIdx.x >> 4) & 1;
   const int tpc = kAppWarps / a.wpt, local = warp / a.wpt, t = blockIdx.x * tpc + local;
