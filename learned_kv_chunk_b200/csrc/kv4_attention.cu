@@ -25,6 +25,7 @@ struct AttnArgs {
   float coef, softcap, cap_log2;
   uint32_t page_magic;  // ceil(2^32 / (page_size / 16)), 0 for a page of 16
   int row_tiles;
+  bool whole;           // a unit is one CTA's
   int run;              // tokens that lie together: the largest power of two in a page, at most a block; list: a block
   // the partial results of units that several CTAs share: two slots a CTA, its first segment's and its last's
   struct Share* share;  // [CTAs]
@@ -44,8 +45,9 @@ struct Share {
 // rows and one piece suffice, 12 of 168 for 16 rows or two pieces.  More query
 // rows of a kv head make more units (tiles of 32 rows, at 255 registers and 8
 // warps an SM, took 1.4 times as long as two of 16 on 32-row calls).  A stage
-// holds a block of four tiles of 32 tokens; the consumers take a segment's tiles
-// as they come free.
+// holds a block of four tiles of 32 tokens; the consumers take a segment's tiles in
+// turn (as they came free took 249 us where this takes 254, 8 x 131072 tokens, but
+// summed in another order each time).
 constexpr int kTok = 32;
 constexpr int kBlock = 128;  // tokens of a stage, the unit in which work is shared out
 constexpr int kTiles = kBlock / kTok;
@@ -205,7 +207,7 @@ __device__ __forceinline__ Range row_range(const AttnArgs& a, int b) {
     r.to = r.len;
   }
   r.blocks = max(1, (r.to - r.from + kBlock - 1) / kBlock);
-  r.cost = r.blocks + kUnitCost;
+  r.cost = a.whole ? 1 : r.blocks + kUnitCost;
   return r;
 }
 
@@ -234,9 +236,15 @@ struct Walk {
   // the current segment: blocks [i0, i1) of a unit; i1 = i0 where only a unit's extra cost lies in the range
   int unit, i0, i1;
   int64_t next_w;
-  __device__ __forceinline__ void segment() {
+  __device__ __forceinline__ void segment(bool whole) {
     const int64_t x = w - base * units;
     unit = (int)div_small(x, rg.cost);
+    if (whole) {
+      next_w = w + 1;
+      i0 = 0;
+      i1 = rg.blocks;
+      return;
+    }
     const int x0 = (int)(x - (int64_t)unit * rg.cost), x1 = (int)min((int64_t)rg.cost, x0 + (end - w));
     next_w = w + (x1 - x0);
     i0 = min(x0, rg.blocks);
@@ -250,7 +258,7 @@ struct Walk {
       base += rg.cost;
       rg = row_range<LIST>(a, ++b);
     }
-    segment();
+    segment(a.whole);
   }
 };
 
@@ -269,9 +277,9 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int64_t sums[kWarps + 1], found[2];
   __shared__ float2 sml[2][kRows];
+  __shared__ float scoef[kRows];
   __shared__ int abort_flag;
   __shared__ int4 place[kTiles];  // of a tile in a stage: its halves' codes and scales
-  __shared__ uint32_t next_tile;  // of the segment, after one for each consumer
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.n_q / a.c.n_heads;
 
@@ -285,7 +293,6 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
         mbar_init(&empty[i], kTiles);
       }
       abort_flag = 0;
-      next_tile = kWarps;
       for (int i = 0; i < kTiles; ++i) {
         const int t0 = kTok * i, t1 = t0 + 16, s0 = t0 / a.run, s1 = t1 / a.run;
         place[i] = make_int4(s0 * a.run * kKvBytes + (t0 - s0 * a.run) * kKvCodeBytes,
@@ -358,12 +365,12 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       }
     }
     if (!mine_to_do) {
-      if (threadIdx.x == 0) a.share[blockIdx.x].b = -1;
+      if (threadIdx.x == 0 && !a.whole) a.share[blockIdx.x].b = -1;
       return;
     }
-    wk.segment();
+    wk.segment(a.whole);
     const int64_t n_cta = min((int64_t)gridDim.x, total);
-    if (threadIdx.x == 32) {
+    if (threadIdx.x == 32 && !a.whole) {
       // the CTAs c with total * c / n_cta <= x own block x: the last of them is ((x + 1) * n_cta - 1) / total
       Share sh = {-1, wk.unit, 0, 0};
       const int64_t w0 = wk.base * wk.units + (int64_t)wk.unit * wk.rg.cost, w1 = w0 + wk.rg.blocks;
@@ -523,19 +530,23 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
     const auto low_of = [&](int p) { return a.window > 0 ? max(rg.start, p - a.window + 1) : rg.start; };
     const int lo_first = low_of(p_first), lo_last = low_of(p_last);
 
-    // the queries: row g of each tile, dims 32t .. 32t+31, as f16 pieces of q * 2^-e, |.| < 2^8
+    // the queries: row g of each tile, dims 32t .. 32t+31, as f16 pieces of q * 2^-e, |.| < 2^8.  One tile: every
+    // warp keeps them; more: a warp a tile puts them into shared memory
     uint32_t qf[kQReg ? P : 1][8][2];
     float coef[NT][2];            // of columns 2t, 2t + 1: scale * 2^e (* log2 e without a cap)
     float slope[NT][2];
     int pq[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
+    const auto row_at = [&](int r, int& tq) {  // query row r of the segment: its token, and its head
+      tq = (r0 + r) / G;
+      return kh * G + (r0 + r - tq * G);
+    };
+    if (kQReg || warp < NT) {
+      const int nt = kQReg ? 0 : warp, r = nt * 8 + g;
       float v[32];
       if (r < rows) {
-        const int tq = (r0 + r) / G;
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)wk.b * a.Tq + tq) * a.q_stride +
-                     (kh * G + (r0 + r - tq * G)) * kKvDim + 32 * t;
+        int tq;
+        const int head = row_at(r, tq);
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)wk.b * a.Tq + tq) * a.q_stride + head * kKvDim + 32 * t;
 #pragma unroll
         for (int i = 0; i < 4; ++i) load8(q + 8 * i, *reinterpret_cast<float(*)[8]>(v + 8 * i));
       } else {
@@ -550,8 +561,12 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       const int e = max(-110, min(120, (int)(__float_as_uint(m) >> 23) - 127 - 7));  // m * 2^-e in [2^7, 2^8)
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       const float c = a.coef * __uint_as_float((uint32_t)(127 + e) << 23);
-      coef[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-      coef[nt][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+      if constexpr (kQReg) {
+        coef[0][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+        coef[0][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+      } else if (t == 0) {
+        scoef[r] = c;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t hi[2], lo[2];
@@ -566,22 +581,27 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           qf[0][j][0] = hi[0];
           qf[0][j][1] = hi[1];
           if constexpr (P == 2) {
-            qf[1][j][0] = lo[0];
-            qf[1][j][1] = lo[1];
+            qf[P - 1][j][0] = lo[0];
+            qf[P - 1][j][1] = lo[1];
           }
-        } else if (warp == nt % kWarps) {
+        } else {
           sq[((nt * P) * 8 + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
           if constexpr (P == 2) sq[((nt * P + 1) * 8 + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = min(nt * 8 + 2 * t + i, rows - 1), tq = (r0 + rr) / G;
-        pq[nt][i] = len - a.Tq + tq;
-        slope[nt][i] = a.slopes ? __ldg(a.slopes + kh * G + (r0 + rr - tq * G)) * kLog2e : 0.f;
-      }
     }
     if constexpr (!kQReg) named_barrier<32 * kWarps>();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * t + i;
+        int tq;
+        const int head = row_at(min(r, rows - 1), tq);
+        pq[nt][i] = len - a.Tq + tq;
+        slope[nt][i] = a.slopes ? __ldg(a.slopes + head) * kLog2e : 0.f;
+        if constexpr (!kQReg) coef[nt][i] = scoef[r];
+      }
 
     // the running maximum is kLift - base; lim is -infinity until the row has seen something
     float o[NT][8][4], base[NT][2], lim[NT][2], l[NT][2];
@@ -804,9 +824,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       }
     };
     const int n_tiles = (wk.i1 - wk.i0) * kTiles;
-    for (int tile_at = warp; tile_at < n_tiles;) {
-      uint32_t after = 0;
-      if (lane == 0) after = atomicAdd(&next_tile, 1u);
+    for (int tile_at = warp; tile_at < n_tiles; tile_at += kWarps) {
       const uint32_t blk = blocks_done + (uint32_t)(tile_at / kTiles), stage = blk % kStages;
       const int in_stage = tile_at % kTiles;
       St& st = ring[stage];
@@ -848,7 +866,6 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
       }
-      tile_at = (int)__shfl_sync(0xffffffffu, after, 0);
     }
     blocks_done += (uint32_t)(wk.i1 - wk.i0);
 
@@ -918,7 +935,6 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       }
     }
     slot = 1;
-    if (threadIdx.x == 0) next_tile = kWarps;
     named_barrier<32 * kWarps>();  // the shared memory is used again
   }
 }
@@ -1007,10 +1023,12 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Attn
 // however the rows' lengths differ.
 struct AttnPlan {
   int nt, row_tiles, grid;
-  bool wide;  // few units: each is shared by many CTAs
+  bool whole;  // a unit is one CTA's: no parts to merge
+  bool wide;   // few units: each is shared by many CTAs
 };
 
 constexpr int kSms = 148;
+constexpr int kWholeBlocks = 4;
 
 AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   AttnPlan p;
@@ -1021,7 +1039,11 @@ AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   if (!d->idx && d->window > 0)  // a row reaches back window + Tq - 1 from the last token, from a multiple of 128
     tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kBlock - 1);
   const int64_t units = (int64_t)c->B * c->n_kv_heads * p.row_tiles;
-  p.grid = (int)std::min<int64_t>(units * ((tokens + kBlock - 1) / kBlock), kSms * kCtas);
+  // Up to 512 tokens a CTA does a whole unit, which saves the merge and its launch (one row of 500 tokens and 8 kv
+  // heads: 12.1 us, shared out 12.4; of 1001 tokens: 14.5 and 12.4).
+  const int64_t blocks = (tokens + kBlock - 1) / kBlock;
+  p.whole = blocks <= kWholeBlocks;
+  p.grid = (int)std::min<int64_t>(p.whole ? units : units * blocks, kSms * kCtas);
   p.wide = 8 * units <= p.grid;
   return p;
 }
@@ -1032,6 +1054,7 @@ struct AttnSpace {
   size_t total() const { return share + ml + o; }
 };
 AttnSpace space_of(const AttnPlan& p) {
+  if (p.whole) return {16, 0, 0};
   const size_t rows = (size_t)p.grid * 2 * 8 * p.nt;
   return {((size_t)p.grid * sizeof(Share) + 15) / 16 * 16, rows * sizeof(float2), rows * kKvDim * sizeof(float)};
 }
@@ -1134,6 +1157,7 @@ extern "C" fm_status fm_kv4_attention(const fm_kv4_cache* c, const fm_kv4_attn_d
   const int q16 = c->page_size / 16;
   a.page_magic = q16 == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + q16 - 1) / q16);
   a.row_tiles = p.row_tiles;
+  a.whole = p.whole;
   a.run = d->idx ? kBlock : std::min(c->page_size & -c->page_size, kBlock);
   uint8_t* at = static_cast<uint8_t*>(ws);
   a.share = reinterpret_cast<Share*>(at);
@@ -1143,7 +1167,7 @@ extern "C" fm_status fm_kv4_attention(const fm_kv4_cache* c, const fm_kv4_attn_d
     using T = std::remove_pointer_t<decltype(tag)>;
     const fm_status s = d->idx ? launch_attn_nt<T, true>(a, p.nt, p.grid, stream)
                                : launch_attn_nt<T, false>(a, p.nt, p.grid, stream);
-    if (s != FM_OK || p.grid == 1) return s;
+    if (s != FM_OK || p.whole || p.grid == 1) return s;
     const cudaError_t e =
         p.wide ? launch_overlapped(kv4_combine_kernel<T, true>, dim3(p.grid - 1, 8 * p.nt), dim3(kCombineThreads), 0,
                                    stream, a, 8 * p.nt)

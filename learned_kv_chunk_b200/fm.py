@@ -595,14 +595,15 @@ def _where(stream, first, *others):
     return index, stream.cuda_stream, stream
 
 
-def _new(make, like, shape, dtype, side):
-    """make = torch.empty or torch.zeros, on like's device; from the side
+def _new(like, shape, dtype, side, zero=False):
+    """A tensor on like's device, empty or of zeros; from the side
     stream's own pool where the call runs on one (its memory may then be used
     there at once) and recorded on the current stream, where the caller goes on."""
+    make = like.new_zeros if zero else like.new_empty
     if side is None:
-        return make(shape, dtype=dtype, device=like.device)
+        return make(shape, dtype=dtype)
     with torch.cuda.stream(side):
-        t = make(shape, dtype=dtype, device=like.device)
+        t = make(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
@@ -716,16 +717,16 @@ def fm_kv4_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pag
     if q is not None:
         n_q, qs = q.shape[1], _heads(q, T, "q", k.dtype)
         if q_out is None:
-            q_out = _new(torch.zeros, k, (T, n_q, 128), k.dtype, side)
+            q_out = _new(k, (T, n_q, 128), k.dtype, side, zero=True)
         qos = _heads(q_out, T, "q_out", k.dtype)
         if q_out.shape[1] != n_q:
             raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out without q")
     if values and k_hat is None:
-        k_hat = _new(torch.zeros, k, k.shape, torch.bfloat16, side)
+        k_hat = _new(k, k.shape, torch.bfloat16, side, zero=True)
     if values and v_hat is None:
-        v_hat = _new(torch.zeros, k, k.shape, torch.bfloat16, side)
+        v_hat = _new(k, k.shape, torch.bfloat16, side, zero=True)
     if k_hat is not None:
         _like(k_hat, k.shape, torch.bfloat16, "k_hat")
     if v_hat is not None:
@@ -787,7 +788,7 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     index, raw, side = _where(stream, q, k_pages, v_pages, page_table, kv_len, slopes, kv_start, idx, count, out,
                               workspace)
     if out is None:
-        out = _new(torch.empty, q, q.shape, q.dtype, side)
+        out = _new(q, q.shape, q.dtype, side)
     else:
         _like(out, q.shape, q.dtype, "out")
     if out.numel() == 0:
@@ -800,7 +801,7 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                          128 ** -0.5 if scale is None else float(scale), float(softcap), _addr(slopes), int(window))
     rc, rd = ctypes.byref(cache), ctypes.byref(d)
     if workspace is None:
-        workspace = _new(torch.empty, q, max(16, _lib.fm_kv4_attention_workspace_bytes(rc, rd)), torch.uint8, side)
+        workspace = _new(q, max(16, _lib.fm_kv4_attention_workspace_bytes(rc, rd)), torch.uint8, side)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _run(index, "fm_kv4_attention", _lib.fm_kv4_attention, rc, rd, workspace.data_ptr(), workspace.numel(), raw)
@@ -861,15 +862,15 @@ def fm_add_rmsnorm_fp8(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
         raise ValueError("group must be 128 or H")
     index, raw, side = _where(stream, x, residual, gain, sum_out, codes, scales)
     if sum_out is None:
-        sum_out = _new(torch.empty, x, (T, H), x.dtype, side)
+        sum_out = _new(x, (T, H), x.dtype, side)
     else:
         _like(sum_out, (T, H), x.dtype, "sum_out")
     if codes is None:
-        codes = _new(torch.empty, x, (T, H), torch.float8_e4m3fn, side)
+        codes = _new(x, (T, H), torch.float8_e4m3fn, side)
     else:
         _like(codes, (T, H), codes.dtype if codes.dtype == torch.uint8 else torch.float8_e4m3fn, "codes")
     if scales is None:
-        scales = _new(torch.empty, x, (T, H // group), torch.float32, side)
+        scales = _new(x, (T, H // group), torch.float32, side)
     else:
         _like(scales, (T, H // group), torch.float32, "scales")
     if T == 0:
