@@ -515,7 +515,7 @@ fm_status fm_rope_frequencies(const fm_config* cfg, double* inv_freq_host);
  * the one to fp32; a 16-bit query is rounded from within 1.5 units of fp32. */
 typedef struct fm_kv4_append_desc {
   int dtype;                  /* FM_F32, FM_BF16, FM_F16: of k, v, q and q_out */
-  int T;                      /* tokens, >= 1 */
+  int T;                      /* tokens, 1..2^30 */
   int n_q_heads;              /* heads of q, 1..1024; ignored when q is NULL */
   const void* k;              /* [T, n_kv_heads, 128] device; the heads of a token are packed */
   const void* v;
@@ -592,7 +592,7 @@ fm_status fm_kv4_attention(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d,
  * [0, N) is padding: nothing is written.  Two tokens of one call must not
  * name the same record.
  * k [T, L, 128] device, 16-byte aligned, token_stride elements between tokens
- * (times the element size: a multiple of 16); 1 <= L <= 4; comp_k: array of L
+ * (times the element size: a multiple of 16); 1 <= T <= 2^30; 1 <= L <= 4; comp_k: array of L
  * device pointers (host array), 4-byte aligned, row b at + b *
  * row_stride_bytes (a multiple of 4, >= N * 132); positions [T] int64 and
  * inv_freq [rope_dim / 2] fp64 device with rope_dim 64 or 128. */

@@ -5,19 +5,27 @@
 //
 // Mathematics.  A head of 128 dimensions belongs to 16 lanes, 8 consecutive
 // dimensions each.  Rotation pairs (D - rd + j, D - rd/2 + j) lie rd/16 lanes
-// apart, so one shuffle brings a lane its partners.
-//   * A rotated value is x1 c - x2 s with c, s in fp32 and x of 8, 11 or 24
+// apart, so a shuffle brings a lane its partners; its own cosines and sines stay
+// in registers for all heads of the token.
+//   * A rotated key value is x1 c - x2 s with c, s in fp32 and x of 8, 11 or 24
 //     bits: each product is split into its fp32 rounding and the exact rest
 //     (one fma), the two are added as a pair, and the pair is rounded once to
 //     fp32 "to odd": truncated, the last bit set if anything was cut off.  A
 //     number rounded to odd compares with any border of fewer bits as the
 //     exact one does and rounds to any shorter type as the exact one does, so
-//     codes, scales and narrow queries are those of the exact rotation.  Plain
-//     fp32 would move one value in about ten million across a code's border,
-//     by a whole step of the 4-bit type.
+//     codes and scales are those of the exact rotation.  Plain fp32 would move
+//     one value in about ten million across a code's border, by a whole step of
+//     the 4-bit type.
 //   * Scale: the least power of two 2^e with max|x| <= 6 * 2^e (6 is the
 //     largest e2m1 value), read from the exponent and mantissa bits of the
 //     group's maximum; x * 2^-e is exact.
+//
+// What bounds them.  Small calls: the chain of loads (position, page, record) and
+// the launch, 4.3 us for 64 tokens of 80 heads and for 64 tokens of three indexer
+// keys.  Prompts: the instructions of the rotation and the transform, issued in
+// four of five cycles.  8192 tokens of 48 heads (210 MB read and written): 55 us,
+// 3.8 TB/s, where a copy would take 32; 32768 tokens of three indexer keys
+// (39 MB): 21 us, where a copy would take 6.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -27,6 +35,7 @@
 namespace fm {
 namespace {
 
+constexpr int kMaxTokens = 1 << 30;           // of a call: a CTA's token indices stay within 32 bits
 constexpr int kAppThreads = 256;              // 16 heads of 16 lanes each
 constexpr int kAppUnits = kAppThreads / 16;
 constexpr int kAppWarps = kAppThreads / 32;
@@ -423,7 +432,8 @@ using namespace fm;
 
 extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_desc* d, cudaStream_t stream) {
   if (fm_status s = check_kv4_cache(c)) return s;
-  if (!d || !d->k || !d->v || !d->seq || !d->pos || d->T < 1 || !dtype_ok(d->dtype)) return FM_ERR_INVALID_ARG;
+  if (!d || !d->k || !d->v || !d->seq || !d->pos || d->T < 1 || d->T > kMaxTokens || !dtype_ok(d->dtype))
+    return FM_ERR_INVALID_ARG;
   if (d->q && (!d->q_out || d->n_q_heads < 1 || d->n_q_heads > 1024)) return FM_ERR_INVALID_ARG;
   if (d->rope_dim != 0 && d->rope_dim != 64 && d->rope_dim != 128) return FM_ERR_UNSUPPORTED;
   if (d->rope_dim && !d->inv_freq) return FM_ERR_INVALID_ARG;
@@ -457,7 +467,7 @@ extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_de
     using T = std::remove_pointer_t<decltype(tag)>;
     return by_rope_dim(d->rope_dim, [&](auto rd) {
       // Warps a token: as few as leave two CTAs an SM (a token's setup is then shared by more heads: 8192 tokens of
-      // 48 heads take APPEND_8 us with eight warps each, APPEND_2 with two), eight where tokens are few, and then its
+      // 48 heads take 68 us with eight warps each, 60 with four or two, 64 with one), eight where tokens are few, and then its
       // heads over as many CTAs as there are shares of 16, up to four CTAs an SM (64 tokens of 80 heads: 12.5 us in
       // one CTA a token, 4.3 in five).
       const int items = 2 * ((c->n_kv_heads + 1) / 2) + (a.n_q + 1) / 2;
@@ -476,7 +486,7 @@ extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_str
                                      const int32_t* chunk, const int64_t* positions, const double* inv_freq,
                                      int rope_dim, int hadamard, uint8_t* const* comp_k, int64_t row_stride_bytes,
                                      int B, int N, cudaStream_t stream) {
-  if (!k || !row || !chunk || !comp_k || T < 1 || L < 1 || L > kMaxLayers || B < 1 || N < 1 || !dtype_ok(dtype))
+  if (!k || !row || !chunk || !comp_k || T < 1 || T > kMaxTokens || L < 1 || L > kMaxLayers || B < 1 || N < 1 || !dtype_ok(dtype))
     return FM_ERR_INVALID_ARG;
   if (rope_dim != 0 && rope_dim != 64 && rope_dim != 128) return FM_ERR_UNSUPPORTED;
   if (rope_dim && (!positions || !inv_freq)) return FM_ERR_INVALID_ARG;
@@ -500,7 +510,7 @@ extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_str
   a.row_stride = row_stride_bytes;
   a.T = T; a.L = L; a.B = B; a.N = N;
   a.hadamard = hadamard != 0;
-  // two CTAs an SM and more with a token a half-warp: 32768 tokens of three layers take INDEX_1 us (INDEX_L with a
+  // two CTAs an SM and more with a token a half-warp: 32768 tokens of three layers take 21 us (28 with a
   // half-warp a key); fewer tokens spread their layers
   a.spread = (int64_t)T >= 2 * 148 * kAppUnits ? 1 : L;
   const int per = kAppUnits / a.spread;

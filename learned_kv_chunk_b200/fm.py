@@ -620,6 +620,13 @@ def _run(index, name, fn, *args):
         raise FMError(status, name)
 
 
+def _i32(value, name: str) -> int:
+    value = int(value)
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -756,6 +763,7 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     visible position), idx / count (fm_compact_mask's list: only the kept
     positions are read).  max_len bounds kv_len where the caller knows it.
     Returns the output in q's type and shape; 0 for a query that sees nothing."""
+    window, max_len = _i32(window, "window"), None if max_len is None else _i32(max_len, "max_len")
     shape, st = q.shape, q.stride()
     if len(shape) not in (3, 4) or shape[-1] != 128 or q.dtype not in DTYPES:
         raise ValueError("q must be [B, heads, 128] or [B, Tq, heads, 128] fp32, bf16 or fp16")
@@ -795,10 +803,10 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         return out
     if idx is not None and max_sel == 0:
         raise ValueError("idx has no entries")
-    bound = cache.max_pages * cache.page_size if max_len is None else int(max_len)
+    bound = cache.max_pages * cache.page_size if max_len is None else max_len
     d = fm_kv4_attn_desc(DTYPES[q.dtype], Tq, n_q, q.data_ptr(), qs, out.data_ptr(), kv_len.data_ptr(),
                          _addr(kv_start), bound, _addr(idx), _addr(count), max_sel,
-                         128 ** -0.5 if scale is None else float(scale), float(softcap), _addr(slopes), int(window))
+                         128 ** -0.5 if scale is None else float(scale), float(softcap), _addr(slopes), window)
     rc, rd = ctypes.byref(cache), ctypes.byref(d)
     if workspace is None:
         workspace = _new(q, max(16, _lib.fm_kv4_attention_workspace_bytes(rc, rd)), torch.uint8, side)

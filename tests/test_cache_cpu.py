@@ -68,7 +68,7 @@ def test_bad_caches_are_refused(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(seq=None), INVALID), (dict(pos=None), INVALID),
-    (dict(T=0), INVALID), (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID), (dict(k_stride=1016), INVALID),
+    (dict(T=0), INVALID), (dict(T=(1 << 30) + 1), INVALID), (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID), (dict(k_stride=1016), INVALID),
     (dict(v_stride=0), INVALID), (dict(rope_dim=32), UNSUP), (dict(inv_freq=None), INVALID),
     (dict(q=FAKE, n_q_heads=32, q_stride=4096, q_out_stride=4096), INVALID),  # no q_out
     (dict(q=FAKE, q_out=FAKE + 4096, n_q_heads=0, q_stride=4096, q_out_stride=4096), INVALID),
@@ -124,7 +124,7 @@ def test_bad_index_appends_are_refused():
         return f(k, dtype, stride, T, L, row, chunk, positions, freq, rd, had, keys, row_stride, B, N, None)
 
     for kw, status in [(dict(k=None), INVALID), (dict(row=None), INVALID), (dict(chunk=None), INVALID),
-                       (dict(keys=None), INVALID), (dict(T=0), INVALID), (dict(L=0), INVALID), (dict(L=5), INVALID),
+                       (dict(keys=None), INVALID), (dict(T=0), INVALID), (dict(T=2147483647), INVALID), (dict(L=0), INVALID), (dict(L=5), INVALID),
                        (dict(B=0), INVALID), (dict(N=0), INVALID), (dict(dtype=9), INVALID), (dict(rd=48), UNSUP),
                        (dict(positions=None), INVALID), (dict(freq=None), INVALID), (dict(stride=380), INVALID),
                        (dict(row_stride=132 * 7), INVALID), (dict(k=FAKE + 4), ALIGN), (dict(stride=385), ALIGN),
@@ -184,6 +184,10 @@ def test_the_binding_refuses_host_tensors_and_shapes():
     lens = torch.ones(1, dtype=torch.int32)
     with pytest.raises(ValueError):
         fm.fm_kv4_attention(k, pages, pages, table, lens)
+    cuda_free = [k, pages, pages, table, lens]
+    for kw in (dict(window=1 << 32), dict(max_len=-(1 << 33)), dict(window=(1 << 32) + 5)):
+        with pytest.raises(ValueError, match="32 bits"):  # a number that 32 bits would cut to another
+            fm.fm_kv4_attention(*cuda_free, **kw)
     with pytest.raises(ValueError):
         fm.fm_kv4_attention(k.double(), pages, pages, table, lens)
     with pytest.raises(ValueError):

@@ -461,6 +461,35 @@ def test_attention_is_the_same_for_every_bound_and_run():
     check_attention(o, q.view(3, 1, 8, 128), kp, vp, table, [100, 10, 100], 16)
 
 
+@pytest.mark.parametrize("window", [256, 257, 1 << 30, (1 << 31) - 1])
+def test_attention_windows_at_and_past_the_row(window):
+    rng = np.random.default_rng(22)
+    run_attention(rng, [257, 3, 0, 256], 4, 2, Tq=2, window=window)
+    run_attention(rng, [257, 3, 0, 256], 4, 2, Tq=2, window=window, kv_start=[(1 << 31) - 1, 0, 7, 100])
+
+
+@pytest.mark.parametrize("B", [33, 200])
+def test_attention_many_rows_share_their_ctas(B):
+    """More rows than lanes find their places by the block's scan; short and long
+    rows share CTAs, and rows of nothing still get their zeros."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 700, B)
+    lens[::7] = 0
+    lens[5] = 1500
+    run_attention(rng, [int(n) for n in lens], 2, 2, dtype="fp32")
+    run_attention(rng, [int(n) for n in lens], 12, 1, dtype="bf16", Tq=2, page=64)
+    run_attention(rng, [int(min(n, 400)) for n in lens], 2, 1)  # short enough for a CTA a unit
+
+
+def test_attention_one_long_row_over_all_ctas():
+    """One kv head: every CTA has a part of the only unit, or of the two units of
+    a second tile of query rows."""
+    rng = np.random.default_rng(23)
+    for Hq in (4, 20):
+        run_attention(rng, [60000], Hq, 1, page=128)
+        run_attention(rng, [40001], Hq, 1, page=48, dtype="fp32")
+
+
 def test_attention_workspace_is_enough_and_not_overrun():
     rng = np.random.default_rng(20)
     lens = [2500, 1300]
