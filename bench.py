@@ -57,12 +57,13 @@ def parse():
     ap.add_argument("--decode-rows", type=int, default=64,
                     help="--path decode: rows of the 262144-chunk workload (64 is the bench line; fewer "
                          "give a small case for profiling)")
-    ap.add_argument("--path", default="retrieve", choices=["retrieve", "recall", "level2", "decode"],
+    ap.add_argument("--path", default="retrieve", choices=["retrieve", "recall", "level2", "decode", "cache"],
                     help="retrieve: the scoring path (default); recall: keep mask -> index lists -> "
                          "gather of the kept chunks' records into a resident buffer; level2: the "
                          "per-step top-512 over a resident set of 4096 chunks per row, one CUDA graph; "
                          "decode: the toy sparse decode loop (retrieval every 64 steps, attention over the "
-                         "kept chunks every step)")
+                         "kept chunks every step); cache: a decode step over the 4-bit paged cache "
+                         "(residual norm, appends, retrieval, attention over the kept tokens)")
     return ap.parse_args()
 
 
@@ -671,6 +672,101 @@ def run_decode(args):
             "gpu_launches": launches, "clocks": sampler.summary()}
 
 
+# --------------------------------------------------------------- cache path
+def run_cache(args):
+    """A decode step over the 4-bit paged cache, 8 rows of 65536 tokens (the
+    retriever's 8-row workload): the residual norm with its 8-bit output, the
+    new token's keys, values, queries and indexer keys appended, the retrieval
+    (top-512 of all chunks), and the attention over the kept tokens.  The
+    projections between them are the model's and are not timed.  The attention
+    over the whole cache is also timed alone."""
+    from learned_kv_chunk_b200 import fm
+
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    wl = G.WORKLOADS[1]
+    inp = G.make_query_inputs(wl)
+    B, N, L, K, Hq, Hkv, page = wl.B, wl.N, G.N_LAYERS, wl.top_k, 64, 8, 64
+    r = fm.Retriever(inp.weights, device=0, max_batch=B, q_pieces=args.q_pieces)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(wl.seed(5))
+    q, _ = r.fm_query_prep(inp.hidden.to(dev), inp.positions.to(dev))
+    plant = q[:, :, 0, :].permute(1, 0, 2).contiguous().cpu()
+    keys = G.make_keys(wl.seed(G.SEED_KEYS), [int(x) for x in inp.n_valid], N, L, plant, device=dev)
+    per = N // page
+    table = torch.randperm(B * per, generator=gen, device=dev).to(torch.int32).view(B, per)
+    pools = []
+    for _ in range(2):
+        p = torch.randint(0, 256, (B * per, Hkv, page * fm.FM_KV4_TOKEN_BYTES), generator=gen, device=dev,
+                          dtype=torch.uint8)
+        p[:, :, page * 64:] = torch.randint(123, 127, (B * per, Hkv, page * 4), generator=gen, device=dev,
+                                            dtype=torch.uint8)
+        pools.append(p)
+    kp, vp = pools
+    freq = fm.fm_rope_frequencies(dev)
+    seq = torch.arange(B, device=dev, dtype=torch.int32)
+    pos = torch.full((B,), N - 1, device=dev, dtype=torch.int64)  # the step's token is the row's last
+    chunk, positions = pos.int(), 4 * pos
+    kv_len = torch.full((B,), N, device=dev, dtype=torch.int32)
+    qkv = torch.randn(B, Hq + 2 * Hkv, 128, generator=gen, device=dev).bfloat16()
+    ik = torch.randn(B, L, 128, generator=gen, device=dev).bfloat16()
+    hidden, resid = inp.hidden.to(dev), torch.randn(B, G.HIDDEN, generator=gen, device=dev)
+    idx = torch.empty(B, K, device=dev, dtype=torch.int32)
+    count = torch.empty(B, device=dev, dtype=torch.int32)
+
+    def step():
+        h, _, _ = fm.fm_add_rmsnorm_fp8(hidden, resid)
+        qr, _, _ = fm.fm_kv4_append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], kp, vp, table, seq, pos, inv_freq=freq,
+                                    q=qkv[:, :Hq])
+        fm.fm_index_append(ik, keys, seq, chunk, inv_freq=freq, positions=positions)
+        _, keep, _ = r.retrieve(h, keys, positions, kv_len, wl.mode, K)
+        fm.fm_compact_mask(keep, K, idx=idx, count=count)
+        return qr, fm.fm_kv4_attention(qr, kp, vp, table, kv_len, idx=idx, count=count)
+
+    stream = torch.cuda.current_stream()
+    for _ in range(max(3, args.warmup)):
+        qr, _ = step()
+    torch.cuda.synchronize()
+    r.fm_sync_status()
+    sampler = ClockSampler(0)
+    launches0 = fm.fm_launch_count()
+    with sampler:
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record(stream)
+        for _ in range(args.steps):
+            step()
+        b.record(stream)
+        torch.cuda.synchronize()
+        t_step = a.elapsed_time(b) / args.steps
+        launches = fm.fm_launch_count() - launches0
+        l2 = torch.cuda.get_device_properties(dev).L2_cache_size
+        flush_buf = torch.empty(max(2 * l2, 1 << 28) // 4, device=dev, dtype=torch.float32)
+        t_attn = _timed_flushed(lambda: fm.fm_kv4_attention(qr, kp, vp, table, kv_len), 20, flush_buf, stream)
+        t_kept = _timed_flushed(lambda: fm.fm_kv4_attention(qr, kp, vp, table, kv_len, idx=idx, count=count), 20,
+                                flush_buf, stream)
+    r.fm_sync_status()
+    hbm_peak, peak_kind = peaks()
+    attn_bytes = B * Hkv * N * 2 * fm.FM_KV4_TOKEN_BYTES + 2 * B * Hq * 128 * 2
+    ach = attn_bytes / (t_attn / 1e3) / 1e9
+    r.close()
+    return {"metric": "decode tokens/sec over the 4-bit paged cache (retrieval and attention over the kept tokens "
+                      "every step)",
+            "value": B / (t_step / 1e3), "unit": "tokens/s", "n_gpus": 1, "steps": args.steps,
+            "warmup": max(3, args.warmup), "ms_per_step": t_step, "higher_is_better": True, "scaling": "weak",
+            "vs_baseline": None, "dtype": "bf16 queries, e2m1 cache, e4m3 indexer keys",
+            "data": "synthetic (seeded generator, random-init weights)",
+            "config": {"workload": f"cache_B{B}_N{N}_top{K}", "rows": B, "tokens_per_row": N, "kept_per_row": K,
+                       "query_heads": Hq, "kv_heads": Hkv, "page_size": page,
+                       "l2": "inputs larger than L2 (0.21 GB of indexer keys a step); attention timed alone after a "
+                             "256 MB L2 flush"},
+            "attention_kept_ms": round(t_kept, 4),
+            "roofline": {"bound": "hbm", "achieved": round(ach, 1), "peak": hbm_peak, "unit": "GB/s",
+                         "frac": round(ach / hbm_peak, 4), "traffic": None, "peak_kind": peak_kind,
+                         "kernel": "attention over the whole 4-bit cache, L2 flushed before each launch",
+                         "kernel_ms": round(t_attn, 4), "alg_bytes_per_launch": attn_bytes},
+            "gpu_launches": launches, "clocks": sampler.summary()}
+
+
 def recall_oracle_sample(keep, src, K, rows=1):
     """The recall oracle (compaction + gather, plain loops) on the first rows."""
     import oracle.recall as OR
@@ -787,6 +883,10 @@ def main():
     if args.path == "decode":
         if rank == 0:
             print(json.dumps(run_decode(args)), flush=True)
+        return
+    if args.path == "cache":
+        if rank == 0:
+            print(json.dumps(run_cache(args)), flush=True)
         return
     if args.path == "level2":
         if rank == 0:
