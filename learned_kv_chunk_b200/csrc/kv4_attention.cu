@@ -247,6 +247,10 @@ __device__ __forceinline__ uint64_t div_small(uint64_t x, uint64_t y) {
   return ((x | y) >> 32) == 0 ? (uint32_t)x / (uint32_t)y : x / y;
 }
 
+__device__ __forceinline__ void arrive_many(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void named_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
@@ -850,49 +854,74 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
         }
       }
     };
-    const int n_tiles = (wk.i1 - wk.i0) * kTiles;
-    for (int tile_at = warp; tile_at < n_tiles; tile_at += kWarps) {
-      const uint32_t blk = blocks_done + (uint32_t)(tile_at / kTiles), stage = blk % kStages;
-      const int in_stage = tile_at % kTiles;
+    // Tiles in turn; where the warps' registers allow, two at a time as long as there are two for each warp.
+    constexpr int kMost = NT == 1 && P == 1 ? 2 : 1;
+    const int n_tiles = (wk.i1 - wk.i0) * kTiles, n_double = kMost == 2 ? n_tiles / (2 * kWarps) * (2 * kWarps) : 0;
+    for (int x = kMost == 2 && n_double ? 2 * warp : warp; x < n_tiles;) {
+      const int n = kMost == 2 && x < n_double ? 2 : 1;  // tiles from x on, of one block
+      const uint32_t blk = blocks_done + (uint32_t)(x / kTiles), stage = blk % kStages;
+      const int first = x % kTiles;
       St& st = ring[stage];
-      const int j0 = rg.from + wk.i0 * kBlock + tile_at * kTok;  // the tile's first token (list: entry)
+      const int j0 = rg.from + wk.i0 * kBlock + x * kTok;  // the first token (list: entry)
       // a wait that ran out ends the work, not the walk: the barriers below want every warp
       if (ok) ok = mbar_wait_bounded(&full[stage], (blk / kStages) & 1u, &abort_flag, &g_kv4_err);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
-        const int4 pl = place[in_stage];
-        const int mine = (lane < 16 ? pl.y : pl.w) + (lane & 15) * kKvScaleBytes;  // the scales of this lane's token
-        uint32_t kw = *reinterpret_cast<const uint32_t*>(st.k + mine), vw = *reinterpret_cast<const uint32_t*>(st.v + mine);
-        const uint32_t there = LIST ? 0u : st.there >> (in_stage * H);
-        bool whole, any = true;
-        if constexpr (LIST) {
-          const int j = st.pos[in_stage * kTok + lane];
-          whole = __all_sync(0xffffffffu, j >= lo_last && j <= p_first);
-        } else {
-          whole = j0 >= lo_last && j0 + kTok - 1 <= p_first && (there & 3u) == 3u;
-        }
-        if (!whole) {
-          // what no row sees may hold anything: its scales are made harmless
-          const int j = LIST ? st.pos[in_stage * kTok + lane] : (there >> (lane >> 4)) & 1u ? j0 + lane : -1;
-          const bool seen = j >= lo_first && j <= p_last;
-          if (!seen) {
-            kw = vw = 0x7f7f7f7fu;
-            *reinterpret_cast<uint32_t*>(st.k + mine) = kw;
-            *reinterpret_cast<uint32_t*>(st.v + mine) = vw;
+        const uint32_t there = LIST ? 0u : st.there >> (first * H);
+        uint32_t kw[kMost], vw[kMost];  // the scales of this lane's token in each tile
+        int at[kMost];
+        bool clear = true;  // seen whole, and with fast scales
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+          const int tile_i = i < n ? first + i : first;
+          const int4 pl = place[tile_i];
+          at[i] = (lane < 16 ? pl.y : pl.w) + (lane & 15) * kKvScaleBytes;
+          kw[i] = *reinterpret_cast<const uint32_t*>(st.k + at[i]);
+          vw[i] = *reinterpret_cast<const uint32_t*>(st.v + at[i]);
+          clear = clear && fast_scales(kw[i], vw[i]);
+          if constexpr (LIST) {
+            const int j = st.pos[tile_i * kTok + lane];
+            clear = clear && j >= lo_last && j <= p_first;
           }
-          any = __any_sync(0xffffffffu, seen);
-          fence_proxy_async_smem();  // the stage's next copy comes after these
-          __syncwarp();
         }
-        const bool fast = __all_sync(0xffffffffu, fast_scales(kw, vw));
-        if (any) {
-          if (!fast) tile(std::false_type{}, std::false_type{}, st, in_stage, pl, j0, there);
-          else if (whole) tile(std::true_type{}, std::true_type{}, st, in_stage, pl, j0, there);
-          else tile(std::true_type{}, std::false_type{}, st, in_stage, pl, j0, there);
+        if constexpr (!LIST) {
+          const uint32_t all = n == 2 ? 15u : 3u;
+          clear = clear && j0 >= lo_last && j0 + n * kTok - 1 <= p_first && (there & all) == all;
+        }
+        if (__all_sync(0xffffffffu, clear)) {
+#pragma unroll 1
+          for (int i = 0; i < n; ++i)
+            tile(std::true_type{}, std::true_type{}, st, first + i, place[first + i], j0 + i * kTok, there >> (i * H));
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < n; ++i) {
+            // what no row sees may hold anything: its scales are made harmless
+            const int j = LIST ? st.pos[(first + i) * kTok + lane]
+                               : (there >> (i * H + (lane >> 4))) & 1u ? j0 + i * kTok + lane : -1;
+            const bool seen = j >= lo_first && j <= p_last;
+            const int last = kMost - 1;
+            if (!seen) {
+              *reinterpret_cast<uint32_t*>(st.k + (i ? at[last] : at[0])) = 0x7f7f7f7fu;
+              *reinterpret_cast<uint32_t*>(st.v + (i ? at[last] : at[0])) = 0x7f7f7f7fu;
+            }
+            const bool fast = __all_sync(0xffffffffu, !seen || fast_scales(i ? kw[last] : kw[0], i ? vw[last] : vw[0]));
+            const bool whole = __all_sync(0xffffffffu, j >= lo_last && j <= p_first);
+            const bool any = __any_sync(0xffffffffu, seen);
+            __syncwarp();
+            if (any) {
+              const int4 pl = place[first + i];
+              if (!fast) tile(std::false_type{}, std::false_type{}, st, first + i, pl, j0 + i * kTok, there >> (i * H));
+              else if (whole) tile(std::true_type{}, std::true_type{}, st, first + i, pl, j0 + i * kTok, there >> (i * H));
+              else tile(std::true_type{}, std::false_type{}, st, first + i, pl, j0 + i * kTok, there >> (i * H));
+            }
+          }
+          fence_proxy_async_smem();  // the stage's next copy comes after these
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (lane == 0) arrive_many(&empty[stage], n);
       }
+      x += n * kWarps;
+      if (kMost == 2 && n == 2 && x >= n_double) x = n_double + warp;
     }
     blocks_done += (uint32_t)(wk.i1 - wk.i0);
 
