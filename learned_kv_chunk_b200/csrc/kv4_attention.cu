@@ -84,7 +84,7 @@ struct Shape {
   static constexpr int kThreads = 32 * (kWarps + 1);
 };
 constexpr int kCtas = 2;     // that an SM holds
-constexpr int stages(int nt, bool list) { return nt == 1 ? (list ? 5 : 6) : 4; }
+constexpr int stages(int nt) { return nt == 1 ? 5 : 4; }
 
 constexpr float kNoMax = -1e30f;          // the running maximum of a row that has seen nothing
 constexpr float kLazy = 6.f;              // the maximum may be exceeded by 2^6 before the sums are rescaled
@@ -298,15 +298,15 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
   constexpr int kRows = S::kRows, H = 2, kWarps = S::kWarps;  // H: 16-token halves of a tile
   constexpr bool kQReg = NT == 1;
   using St = Stage<LIST>;
-  constexpr int kStages = stages(NT, LIST);
+  constexpr int kStages = stages(NT);
   extern __shared__ __align__(128) uint8_t smem[];
   St* ring = reinterpret_cast<St*>(smem);
-  // the queries, when they are not kept in registers, then the merge's outputs of two warps
+  // the queries, when they are not kept in registers, then the merge's outputs of four warps
   uint2* sq = reinterpret_cast<uint2*>(ring + kStages);
   float* so = reinterpret_cast<float*>(sq + (kQReg ? 0 : NT * P * 8 * 32));
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int64_t sums[kWarps + 1], found[2];
-  __shared__ float2 sml[2][kRows];
+  __shared__ float2 sml[4][kRows];
   __shared__ float scoef[kRows];
   __shared__ int abort_flag;
   __shared__ int4 place[kTiles];  // of a tile in a stage: its halves' codes and scales
@@ -925,7 +925,8 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
     }
     blocks_done += (uint32_t)(wk.i1 - wk.i0);
 
-    // ---- the warps' sums merged in shared memory: two at a time add to the first two, then the second to the first
+    // ---- the warps' sums merged in shared memory: those past the fourth add to the first ones, then all threads add
+    // up the four
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -950,44 +951,49 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           if (g == 0) sml[to][r] = make_float2(M[nt][i], l[nt][i]);
         }
     };
-#pragma unroll 1
-    for (int left = kWarps; left > 1;) {
-      const int n_from = left > 3 ? 2 : 1;
-      left -= n_from;
-      if (warp >= left && warp < left + n_from) put(warp - left);
-      named_barrier<32 * kWarps>();
-      if (warp < n_from) {
+    if (warp >= 4) put(warp - 4);
+    named_barrier<32 * kWarps>();
+    if (warp < kWarps - 4) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = nt * 8 + 2 * t + i;
-            const float* row = so + (warp * kRows + r) * kORow;
-            const float2 ml = sml[warp][r];
-            const float m = fmaxf(M[nt][i], ml.x), f0 = ex2(M[nt][i] - m), f1 = ex2(ml.x - m);
-            M[nt][i] = m;
-            l[nt][i] = l[nt][i] * f0 + ml.y * f1;
+        for (int i = 0; i < 2; ++i) {
+          const int r = nt * 8 + 2 * t + i;
+          const float* row = so + (warp * kRows + r) * kORow;
+          const float2 ml = sml[warp][r];
+          const float m = fmaxf(M[nt][i], ml.x), f0 = ex2(M[nt][i] - m), f1 = ex2(ml.x - m);
+          M[nt][i] = m;
+          l[nt][i] = l[nt][i] * f0 + ml.y * f1;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              const float2 x = *reinterpret_cast<const float2*>(row + 16 * d + 2 * g);
-              o[nt][d][i] = o[nt][d][i] * f0 + x.x * f1;
-              o[nt][d][i + 2] = o[nt][d][i + 2] * f0 + x.y * f1;
-            }
+          for (int d = 0; d < 8; ++d) {
+            const float2 x = *reinterpret_cast<const float2*>(row + 16 * d + 2 * g);
+            o[nt][d][i] = o[nt][d][i] * f0 + x.x * f1;
+            o[nt][d][i + 2] = o[nt][d][i + 2] * f0 + x.y * f1;
           }
-      }
-      named_barrier<32 * kWarps>();
+        }
     }
-    if (warp == 0) put(0);  // all of them write it out
+    named_barrier<32 * kWarps>();
+    if (warp < 4) put(warp);
     named_barrier<32 * kWarps>();
     for (int x = threadIdx.x; x < rows * kKvDim; x += 32 * kWarps) {
       const int r = x / kKvDim, d = x % kKvDim;
-      const float num = so[r * kORow + ((d & 15) >> 1) * 16 + (d >> 4) * 2 + (d & 1)], den = sml[0][r].y;
+      const int at = r * kORow + ((d & 15) >> 1) * 16 + (d >> 4) * 2 + (d & 1);
+      float m = kNoMax, num = 0.f, den = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, sml[i][r].x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 ml = sml[i][r];
+        const float f = ex2(ml.x - m);
+        den = fmaf(f, ml.y, den);
+        num = fmaf(f, so[i * kRows * kORow + at], num);
+      }
       if (complete) {
         store1(static_cast<T*>(a.out) + out_row(a, wk.b, kh, G, r0 + r) * kKvDim + d, den == 0.f ? 0.f : num / den);
       } else {
         const int64_t R = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
         a.part_o[R * kKvDim + d] = num;
-        if (d == 0) a.part_ml[R] = sml[0][r];
+        if (d == 0) a.part_ml[R] = make_float2(m, den);
       }
     }
     slot = 1;
@@ -1159,8 +1165,8 @@ namespace {
 template <class T, int NT, int P, bool LIST>
 fm_status launch_attn(const AttnArgs& a, int grid, cudaStream_t stream) {
   using S = Shape<NT, P>;
-  constexpr int kSmem = stages(NT, LIST) * (int)sizeof(Stage<LIST>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
-                        2 * S::kRows * kORow * (int)sizeof(float);
+  constexpr int kSmem = stages(NT) * (int)sizeof(Stage<LIST>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
+                        4 * S::kRows * kORow * (int)sizeof(float);
   static_assert((kSmem + 2048) * kCtas <= 228 * 1024, "shared memory of an SM, with the static and the reserved parts");
   static PerDeviceOnce once;
   int dev = 0;
