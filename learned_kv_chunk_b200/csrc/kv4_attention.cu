@@ -23,8 +23,10 @@
 // tokens, 8 kv heads: 1.14 GB in 187 us, 6.1 TB/s).  The arithmetic does not hide
 // behind them: 32 tokens of a kv head take 128 conversions, 128 products with the
 // scales, 64 selections and shifts and 32 matrix instructions of a warp, each at
-// two cycles (eight the last), about 640 instructions with the rest, on 14
-// consumer warps an SM: 252 us, 4.5 TB/s.
+// two cycles (eight the last), about 590 instructions with the rest, on 14
+// consumer warps an SM: 240 us, 4.75 TB/s.  In short calls the start counts: a
+// warp's first tile takes 9000 to 12000 cycles where later ones take 2000, with
+// its data there or not, and a change of units 8000 (merge, queries).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -71,9 +73,9 @@ struct Share {
 // rows and one piece suffice, 12 of 168 for 16 rows or two pieces.  More query
 // rows of a kv head make more units (tiles of 32 rows, at 255 registers and 8
 // warps an SM, took 1.4 times as long as two of 16 on 32-row calls).  A stage
-// holds a block of four tiles of 32 tokens; the consumers take a segment's tiles in
-// turn (as they came free took 249 us where this takes 254, 8 x 131072 tokens, but
-// summed in another order each time).
+// holds a block of four tiles of 32 tokens (twice as many stages of two tiles took 251
+// us where this takes 240, 8 x 131072 tokens); the consumers take a segment's tiles in
+// turn (as they came free saved 2 %, but summed in another order each time).
 constexpr int kTok = 32;
 constexpr int kBlock = 128;  // tokens of a stage, the unit in which work is shared out
 constexpr int kTiles = kBlock / kTok;
@@ -854,7 +856,8 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
         }
       }
     };
-    // Tiles in turn; where the warps' registers allow, two at a time as long as there are two for each warp.
+    // Tiles in turn; where the warps' registers allow, two at a time as long as there are two for each warp (one
+    // at a time: 252 us where this takes 240, 8 x 131072 tokens).
     constexpr int kMost = NT == 1 && P == 1 ? 2 : 1;
     const int n_tiles = (wk.i1 - wk.i0) * kTiles, n_double = kMost == 2 ? n_tiles / (2 * kWarps) * (2 * kWarps) : 0;
     for (int x = kMost == 2 && n_double ? 2 * warp : warp; x < n_tiles;) {
