@@ -610,7 +610,8 @@ fm_status fm_index_append(const void* k, int dtype, int64_t token_stride, int T,
  * (formed as z * gain * (448 / max|z * gain|), in fp32).  A group whose largest
  * |z * gain| is below 2^-100 is stored as zeros with scale 0; a row whose sum of
  * squares is not finite in fp32 (a NaN, an infinity, values past 2^63) has NaN
- * scales.
+ * scales; without an eps, one whose squares all round to 0 has infinite ones
+ * where it is not stored as zeros.
  * x, residual [T, H] device, 16-byte aligned, x_stride / residual_stride elements between rows (times
  * the element size: a multiple of 16); gain [H] of the same type; sum_out
  * [T, H] packed or NULL, may be x or residual when that is packed; codes

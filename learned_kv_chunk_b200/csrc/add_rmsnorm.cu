@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(cons
       c[k] = lo | (hi << 16);
     }
     *reinterpret_cast<uint2*>(a.codes + row * a.H + 8 * i) = make_uint2(c[0], c[1]);
-    const float scale = m < kTiny ? 0.f * inv_rms : m * inv_rms * (1.f / 448.f);  // NaN where the row's sum is
+    // NaN where the row's sum is; without an eps a row of zeros has an infinite inv_rms
+    const float scale = m < kTiny && inv_rms == inv_rms ? 0.f : m * inv_rms * (1.f / 448.f);
     if (PER_ROW ? i == 0 : (i & 15) == 0) a.scales[PER_ROW ? row : row * (a.H / kKvDim) + (i >> 4)] = scale;
   }
 }

@@ -688,6 +688,16 @@ def test_norm_in_place_strided_and_odd_rows():
     assert k[4, 0] == 0 and v[4, 130] == pytest.approx(2.0 / math.sqrt(4.0 / 256 + 1e-6), rel=2.0 ** -18)
 
 
+@pytest.mark.parametrize("group", [128, 256])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norm_without_eps_of_zeros_is_zeros(dtype, group):
+    z = torch.zeros(2, 256, device=DEV, dtype=TYPES[dtype])
+    z[1, 7] = 4.0
+    s, c, k = fm.fm_add_rmsnorm_fp8(z, eps=0.0, group=group)
+    assert torch.equal(s, z) and (c[0].float() == 0).all() and (k[0] == 0).all()
+    assert float(c[1, 7]) * float(k[1, 0]) == pytest.approx(16.0, rel=2.0 ** -18) and (k[1, 1:] == 0).all()
+
+
 # -------------------------------------------------------------- a run of them
 
 
