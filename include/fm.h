@@ -564,8 +564,8 @@ typedef struct fm_kv4_attn_desc {
                                  listed twice counts twice, one outside [0, kv_len) not at all */
   const int32_t* count;       /* [B] device, with idx: entries of a row, clamped to [0, max_sel] */
   int max_sel;
-  float scale;                /* finite */
-  float softcap;              /* 0: none; > 0 */
+  float scale;                /* -2^32..2^32 */
+  float softcap;              /* 0: none; 2^-32..2^32 */
   const float* slopes;        /* [n_q_heads] device or NULL */
   int window;                 /* 0: none; > 0 */
 } fm_kv4_attn_desc;

@@ -144,6 +144,21 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// cap * tanh(y) in log2 units = cap - 2 cap / (1 + e^2y), within 2^-22 cap; where the
+// cap is far above the scores (kFarCap), small y by the series of tanh instead
+// (its next term is below 2^-26 y for |y| < 1/4).
+constexpr float kFarCap = 64.f;
+__device__ __forceinline__ float capped(const AttnArgs& a, float y) {
+  return a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(y * (2.f * kLog2e)));
+}
+__device__ __forceinline__ float tanh_near(float y) {
+  const float z = y * y;
+  float p = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
+  p = fmaf(z, p, 2.f / 15.f);
+  p = fmaf(z, p, -1.f / 3.f);
+  return fmaf(y * z, p, y);
+}
+
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -728,13 +743,25 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
+            for (int c = 0; c < 4; ++c)
+              x[h][c] = s[h][nt][c] * (FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1]);
+          if (a.softcap > 0.f) {  // coef holds scale / softcap
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float y = x[h][c];
+                x[h][c] = capped(a, y);
+                if (a.softcap > kFarCap && fabsf(y) < 0.25f) x[h][c] = a.cap_log2 * tanh_near(y);
+              }
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
-              float y = s[h][nt][c] * (FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1]);
-              if (a.softcap > 0.f)  // coef holds scale / softcap: cap * tanh(y) = cap - 2 cap / (1 + e^2y)
-                y = a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(y * (2.f * kLog2e)));
               if (a.slopes)
-                y = fmaf(slope[nt][c & 1], (float)(pos_at(16 * h + 8 * (c >> 1) + tk) - pq[nt][c & 1]), y);
-              x[h][c] = y + base[nt][c & 1];
+                x[h][c] = fmaf(slope[nt][c & 1], (float)(pos_at(16 * h + 8 * (c >> 1) + tk) - pq[nt][c & 1]), x[h][c]);
+              x[h][c] += base[nt][c & 1];
             }
         }
         if constexpr (!FAST) {
@@ -1134,8 +1161,10 @@ fm_status check_attn(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   if (d->Tq > kMaxTq) return FM_ERR_UNSUPPORTED;
   if (d->max_len < 1 || d->max_len > (int64_t)c->max_pages * c->page_size) return FM_ERR_INVALID_ARG;
   if (d->idx && (!d->count || d->max_sel < 1 || d->max_sel > (1 << 30))) return FM_ERR_INVALID_ARG;
-  if (!std::isfinite(d->scale) || !std::isfinite(d->softcap) || d->softcap < 0.f || d->window < 0)
-    return FM_ERR_INVALID_ARG;
+  // within 2^32, and a cap not below 2^-32: then their quotient times a query's power of two is a number
+  constexpr float kMost = 4294967296.f;
+  if (!(std::fabs(d->scale) <= kMost) || d->window < 0) return FM_ERR_INVALID_ARG;
+  if (d->softcap != 0.f && !(d->softcap >= 1.f / kMost && d->softcap <= kMost)) return FM_ERR_INVALID_ARG;
   return FM_OK;
 }
 

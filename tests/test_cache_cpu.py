@@ -99,6 +99,17 @@ def test_bad_attention_calls_are_refused(kw, status):
     assert fm.lib().fm_kv4_attention(ctypes.byref(c), ctypes.byref(d), FAKE, 1 << 40, None) == status
 
 
+@pytest.mark.parametrize("kw,ok", [
+    (dict(scale=2.0 ** 32), True), (dict(scale=-2.0 ** 32), True), (dict(scale=2.0 ** 33), False),
+    (dict(scale=-2.0 ** 33), False), (dict(softcap=2.0 ** 32), True), (dict(softcap=2.0 ** -32), True),
+    (dict(softcap=2.0 ** 33), False), (dict(softcap=2.0 ** -33), False), (dict(softcap=float("inf")), False)])
+def test_attention_scales_and_caps_out_of_range_are_refused(kw, ok):
+    c, d = cache(), attn_desc(**kw)
+    assert (fm.lib().fm_kv4_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(d)) > 0) == ok
+    if not ok:
+        assert fm.lib().fm_kv4_attention(ctypes.byref(c), ctypes.byref(d), FAKE, 1 << 40, None) == INVALID
+
+
 def test_attention_workspace_rules():
     c, d = cache(), attn_desc()
     need = fm.lib().fm_kv4_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(d))

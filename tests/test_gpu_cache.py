@@ -308,6 +308,25 @@ def test_attention_masks_caps_and_biases(dtype, kw, Tq):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("softcap", [65.0, 300.0, 2.0 ** 17, 2.0 ** 32])
+def test_attention_with_a_cap_far_above_the_scores(dtype, softcap):
+    """Such a cap costs no accuracy: the tolerance has no term of the cap."""
+    rng = np.random.default_rng(12)
+    lens, page, kind = [300, 41, 700], 16, TYPES[dtype]
+    for spread in (0.3, 3.0):  # scores of a few units, and of hundreds
+        kp, vp, table = make_cache(rng, lens, 2, page)
+        q = torch.from_numpy(spread * rng.standard_normal((3, 1, 8, 128))).to(kind)
+        o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.asarray(lens, np.int32)), softcap=softcap)
+        k, there = OC.read_cache(kp, table, page)
+        v, _ = OC.read_cache(vp, table, page)
+        ref, _, abs_v, top_v = OC.attention(q.double().numpy(), k, v, there, lens, softcap=softcap)
+        _, err_x, _, _ = OC.attention(q.double().numpy(), k, v, there, lens)
+        w = (2.0 ** -11 if dtype == "bf16" else 2.0 ** -20) + 2.0 ** -23 * (700 / 16 + 16)
+        tol = (2 * 2.0 ** -20 * err_x + w) * abs_v + top_v + half_step(kind) * np.abs(ref) + 1e-37
+        assert (np.abs(o.double().cpu().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("max_sel", [1, 7, 64, 300, 1500])
 @pytest.mark.parametrize("Hq,Hkv,Tq", [(32, 1, 1), (8, 4, 3)])
 def test_attention_over_a_kept_list(dtype, max_sel, Hq, Hkv, Tq):
