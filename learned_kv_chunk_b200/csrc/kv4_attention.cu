@@ -144,9 +144,10 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// cap * tanh(y) in log2 units = cap - 2 cap / (1 + e^2y), within 2^-22 cap; where the
-// cap is far above the scores (kFarCap), small y by the series of tanh instead
-// (its next term is below 2^-26 y for |y| < 1/4).
+// cap * tanh(y) in log2 units = cap - 2 cap / (1 + e^2y), within 2^-22 cap: up to
+// kFarCap 2^-16 of a logit, what 16-bit queries lose anyway.  Above it small y go by the
+// series of tanh (its next term is below 2^-26 y for |y| < 1/4); the test for that
+// costs 3 % (32 rows of up to 8192 tokens with a cap: 53.2 us, 51.5 without).
 constexpr float kFarCap = 64.f;
 __device__ __forceinline__ float capped(const AttnArgs& a, float y) {
   return a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(y * (2.f * kLog2e)));
