@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "kv4.cuh"
+#include "kv4_ring.cuh"
 
 namespace fm {
 namespace {
@@ -76,17 +77,13 @@ struct Share {
 // holds a block of four tiles of 32 tokens (twice as many stages of two tiles took 251
 // us where this takes 240, 8 x 131072 tokens); the consumers take a segment's tiles in
 // turn (as they came free saved 2 %, but summed in another order each time).
-constexpr int kTok = 32;
-constexpr int kBlock = 128;  // tokens of a stage, the unit in which work is shared out
-constexpr int kTiles = kBlock / kTok;
 template <int NT, int P>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = NT == 1 && P == 1 ? 7 : 5;  // consumers
+  static constexpr int kWarps = ring_warps(NT, P);  // consumers
   static constexpr int kThreads = 32 * (kWarps + 1);
 };
 constexpr int kCtas = 2;     // that an SM holds
-constexpr int stages(int nt) { return nt == 1 ? 5 : 4; }
 
 constexpr float kNoMax = -1e30f;          // the running maximum of a row that has seen nothing
 constexpr float kLazy = 6.f;              // the maximum may be exceeded by 2^6 before the sums are rescaled
@@ -316,13 +313,15 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
   constexpr int kRows = S::kRows, H = 2, kWarps = S::kWarps;  // H: 16-token halves of a tile
   constexpr bool kQReg = NT == 1;
   using St = Stage<LIST>;
-  constexpr int kStages = stages(NT);
+  constexpr int kStages = ring_stages(NT), kMost = ring_most(NT, P);
+  static_assert(ring_is_sound<kStages, kWarps, kMost>());
+  using RingT = Ring<kStages>;
   extern __shared__ __align__(128) uint8_t smem[];
   St* ring = reinterpret_cast<St*>(smem);
   // the queries, when they are not kept in registers, then the merge's outputs of four warps
   uint2* sq = reinterpret_cast<uint2*>(ring + kStages);
   float* so = reinterpret_cast<float*>(sq + (kQReg ? 0 : NT * P * 8 * 32));
-  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ uint64_t full[2 * kStages], empty[kStages];
   __shared__ int64_t sums[kWarps + 1], found[2];
   __shared__ float2 sml[4][kRows];
   __shared__ float scoef[kRows];
@@ -338,7 +337,8 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
   {
     if (threadIdx.x == 0) {
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(&full[i], LIST ? 64 : 1);
+        mbar_init(&full[2 * i], LIST ? 64 : 1);
+        mbar_init(&full[2 * i + 1], LIST ? 64 : 1);
         mbar_init(&empty[i], kTiles);
       }
       abort_flag = 0;
@@ -434,20 +434,11 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
     __syncthreads();  // the barriers are there
   }
 
-  int stage = 0;
-  uint32_t phase = 0;
-  const auto advance = [&] {
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1;
-    }
-  };
-
   if (warp == kWarps) {
     // ---- the producer: a stage for every block, as soon as the consumers have left it
     const int scales_at = a.c.page_size * kKvCodeBytes;
     bool ok = true;
-    uint32_t filled = 0;  // stages whose copies are under way
+    uint32_t blk = 0;  // blocks so far
     for (; ok && wk.more(); wk.next(a)) {
       const int kh = wk.unit / a.row_tiles;
       const int32_t* table = a.c.table + wk.b * a.c.table_stride;
@@ -473,6 +464,8 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       look(wk.i0);
       for (int i = wk.i0; i < wk.i1; ++i) {
         const int n = wk.rg.from + i * kBlock;
+        const int stage = RingT::stage(blk);
+        uint64_t* landed = &full[RingT::full(blk)];
         St& st = ring[stage];
         if constexpr (LIST) {
           int pos[kPer], page[kPer];
@@ -482,7 +475,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
             page[e] = pos[e] >= 0 ? __ldg(table + page_index(a, pos[e])) : -1;
           }
           look(i + 1);
-          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, &abort_flag, &g_kv4_err);
+          ok = mbar_wait_bounded(&empty[stage], RingT::empty_parity(blk), &abort_flag, &g_kv4_err);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -490,14 +483,14 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
             if (page[e] < 0 || page[e] >= a.c.n_pages) page[e] = pos[e] = -1;
-            const int64_t blk = max(page[e], 0) * a.c.page_stride;
+            const int64_t from = max(page[e], 0) * a.c.page_stride;
             const int slot = pos[e] >= 0 ? pos[e] - page_index(a, pos[e]) * a.c.page_size : 0;
-            const int64_t off = pos[e] >= 0 ? blk + slot * kKvCodeBytes : -1;
+            const int64_t off = pos[e] >= 0 ? from + slot * kKvCodeBytes : -1;
             st.pos[32 * e + lane] = pos[e];
             if (pos[e] >= 0) {
               const int to = kBlock * kKvCodeBytes + (32 * e + lane) * kKvScaleBytes;
-              cp_async4(st.k + to, kp + blk + scales_at + slot * kKvScaleBytes);
-              cp_async4(st.v + to, vp + blk + scales_at + slot * kKvScaleBytes);
+              cp_async4(st.k + to, kp + from + scales_at + slot * kKvScaleBytes);
+              cp_async4(st.v + to, vp + from + scales_at + slot * kKvScaleBytes);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {  // four lanes an entry's 64 bytes
@@ -509,52 +502,47 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
               }
             }
           }
-          cp_async_arrive(&full[stage]);
-          mbar_arrive(&full[stage]);
+          cp_async_arrive(landed);
+          mbar_arrive(landed);
         } else {
           const int page = ahead[0];
           look(i + 1);
           const bool there = page >= 0 && page < a.c.n_pages;
           const uint32_t runs = __ballot_sync(0xffffffffu, there);
           const uint32_t chunks = __ballot_sync(0xffffffffu, lane * 16 < kBlock && ((runs >> (lane * 16 / a.run)) & 1u));
-          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, &abort_flag, &g_kv4_err);
+          ok = mbar_wait_bounded(&empty[stage], RingT::empty_parity(blk), &abort_flag, &g_kv4_err);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           if (lane == 0) {
             st.there = chunks;
-            mbar_arrive_expect_tx(&full[stage], (uint32_t)__popc(runs) * a.run * kKvBytes * 2);
+            mbar_arrive_expect_tx(landed, (uint32_t)__popc(runs) * a.run * kKvBytes * 2);
           }
           __syncwarp();
           if (there) {
             const int at = n + lane * a.run, slot = at - page_index(a, at) * a.c.page_size;
-            const int64_t blk = page * a.c.page_stride;
+            const int64_t from = page * a.c.page_stride;
             uint8_t* ks = st.k + lane * a.run * kKvBytes;
             uint8_t* vs = st.v + lane * a.run * kKvBytes;
             if (a.run == a.c.page_size) {
-              bulk_g2s(ks, kp + blk, a.run * kKvBytes, &full[stage]);
-              bulk_g2s(vs, vp + blk, a.run * kKvBytes, &full[stage]);
+              bulk_g2s(ks, kp + from, a.run * kKvBytes, landed);
+              bulk_g2s(vs, vp + from, a.run * kKvBytes, landed);
             } else {
               const int codes = a.run * kKvCodeBytes, scales = a.run * kKvScaleBytes;
-              bulk_g2s(ks, kp + blk + slot * kKvCodeBytes, codes, &full[stage]);
-              bulk_g2s(vs, vp + blk + slot * kKvCodeBytes, codes, &full[stage]);
-              bulk_g2s(ks + codes, kp + blk + scales_at + slot * kKvScaleBytes, scales, &full[stage]);
-              bulk_g2s(vs + codes, vp + blk + scales_at + slot * kKvScaleBytes, scales, &full[stage]);
+              bulk_g2s(ks, kp + from + slot * kKvCodeBytes, codes, landed);
+              bulk_g2s(vs, vp + from + slot * kKvCodeBytes, codes, landed);
+              bulk_g2s(ks + codes, kp + from + scales_at + slot * kKvScaleBytes, scales, landed);
+              bulk_g2s(vs + codes, vp + from + scales_at + slot * kKvScaleBytes, scales, landed);
             }
           }
         }
-        filled |= 1u << stage;
-        advance();
+        ++blk;
       }
       if (!ok) break;
     }
-    // copies may be under way only if a wait ran out: they land before the CTA ends
-    if (!ok)
-      for (int i = 0; i < kStages; ++i) {
-        const bool wrapped = i < stage;  // filled in this round
-        if ((filled >> i) & 1u) mbar_drain(&full[i], wrapped ? phase : phase ^ 1, &g_kv4_err);
-      }
+    // the last copies into every stage land before the CTA ends, whichever wait ran out
+    for (uint32_t b = blk > kStages ? blk - kStages : 0; b < blk; ++b) mbar_drain(&full[RingT::full(b)], RingT::full_parity(b), &g_kv4_err);
     return;
   }
 
@@ -886,16 +874,15 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
     };
     // Tiles in turn; where the warps' registers allow, two at a time as long as there are two for each warp (one
     // at a time: 252 us where this takes 240, 8 x 131072 tokens).
-    constexpr int kMost = NT == 1 && P == 1 ? 2 : 1;
-    const int n_tiles = (wk.i1 - wk.i0) * kTiles, n_double = kMost == 2 ? n_tiles / (2 * kWarps) * (2 * kWarps) : 0;
-    for (int x = kMost == 2 && n_double ? 2 * warp : warp; x < n_tiles;) {
-      const int n = kMost == 2 && x < n_double ? 2 : 1;  // tiles from x on, of one block
-      const uint32_t blk = blocks_done + (uint32_t)(x / kTiles), stage = blk % kStages;
+    const TileOrder<kWarps, kMost> order((wk.i1 - wk.i0) * kTiles);
+    for (int x = order.first(warp); x < order.n_tiles; x = order.next(x, warp)) {
+      const int n = order.count(x);  // tiles from x on, of one block
+      const uint32_t blk = blocks_done + (uint32_t)(x / kTiles);
       const int first = x % kTiles;
-      St& st = ring[stage];
+      St& st = ring[RingT::stage(blk)];
       const int j0 = rg.from + wk.i0 * kBlock + x * kTok;  // the first token (list: entry)
       // a wait that ran out ends the work, not the walk: the barriers below want every warp
-      if (ok) ok = mbar_wait_bounded(&full[stage], (blk / kStages) & 1u, &abort_flag, &g_kv4_err);
+      if (ok) ok = mbar_wait_bounded(&full[RingT::full(blk)], RingT::full_parity(blk), &abort_flag, &g_kv4_err);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         const uint32_t there = LIST ? 0u : st.there >> (first * H);
@@ -949,10 +936,8 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           fence_proxy_async_smem();  // the stage's next copy comes after these
         }
         __syncwarp();
-        if (lane == 0) arrive_many(&empty[stage], n);
+        if (lane == 0) arrive_many(&empty[RingT::stage(blk)], n);
       }
-      x += n * kWarps;
-      if (kMost == 2 && n == 2 && x >= n_double) x = n_double + warp;
     }
     blocks_done += (uint32_t)(wk.i1 - wk.i0);
 
@@ -1198,7 +1183,7 @@ namespace {
 template <class T, int NT, int P, bool LIST>
 fm_status launch_attn(const AttnArgs& a, int grid, cudaStream_t stream) {
   using S = Shape<NT, P>;
-  constexpr int kSmem = stages(NT) * (int)sizeof(Stage<LIST>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
+  constexpr int kSmem = ring_stages(NT) * (int)sizeof(Stage<LIST>) + (NT == 1 ? 0 : NT * P * 8 * 32 * (int)sizeof(uint2)) +
                         4 * S::kRows * kORow * (int)sizeof(float);
   static_assert((kSmem + 2048) * kCtas <= 228 * 1024, "shared memory of an SM, with the static and the reserved parts");
   static PerDeviceOnce once;
