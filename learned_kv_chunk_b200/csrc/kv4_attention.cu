@@ -88,6 +88,10 @@ constexpr int kCtas = 2;     // that an SM holds
 constexpr float kNoMax = -1e30f;          // the running maximum of a row that has seen nothing
 constexpr float kLazy = 6.f;              // the maximum may be exceeded by 2^6 before the sums are rescaled
 constexpr float kLift = 8.f;              // weights are held times 2^8: at most 2^14 in f16
+// Where a value's scale passes 2^72 the outputs could leave fp32's range: from such a tile on a segment's sums are
+// held 2^64 lower (and its tiles take the general form, as f16 would not hold such weights).
+constexpr uint32_t kHugeScale = 127 + 72;
+constexpr float kDrop = 64.f;
 constexpr int kORow = 132;         // floats between rows of the warps' outputs in shared memory
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -115,6 +119,17 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
+}
+
+// The lowest code byte of w as a f16 pair.
+__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  return h;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -174,8 +189,12 @@ __device__ int g_kv4_err;  // kDevErrTimeout once a wait of the attention's ran 
 // [113, 139] (2^-14 .. 2^12: what real keys and values have) is FAST: a group's
 // factor is the f16 number of that exponent, (byte - 112) << 10, and its
 // products with a code are exact.  Any other tile takes the general form: each
-// record's factors are relative to its largest scale 2^r, which multiplies the
-// score (keys) or joins the weight's exponent (values).
+// record's factors are relative to its largest scale 2^r.  That multiplies the
+// score (keys); for values it joins the exponent of the weight that goes to the
+// product, and of that only: the running maximum and the sum of weights know no
+// sizes.  A tile's products are relative to its largest weight times size, and
+// join the outputs by one factor a row, so tokens of any size, zeros among them,
+// keep their part in both sums.
 __device__ __forceinline__ bool fast_scales(uint32_t a, uint32_t b) {
   // bytes + 116 in [224, 255] is [108, 139], + 15 in [128, 255] is [113, 240]; a
   // byte that carries into its neighbour fails the first test itself
@@ -197,11 +216,6 @@ __device__ __forceinline__ uint32_t top_scale(uint32_t w) {
   for (int i = 0; i < 4; ++i) r = max(r, byte_of(w, i) == 255u ? 0u : byte_of(w, i));
   return r;
 }
-// A value's size: a record of zeros has none of its own, below 2^-100 none is kept.
-__device__ __forceinline__ uint32_t top_value_scale(uint32_t w) {
-  const uint32_t r = top_scale(w);
-  return r == 0u ? 127u : max(r, 27u);
-}
 // f16 bits of 2^(byte i - r), 0 below 2^-25.
 __device__ __forceinline__ uint32_t group_factor(uint32_t w, int i, uint32_t r) {
   const __half h = __float2half_rn(__int_as_float(max(127 + (int)byte_of(w, i) - (int)r, 0) << 23));
@@ -217,8 +231,6 @@ struct alignas(16) Stage {
   int pos[LIST ? kBlock : 1];  // the entries' positions, -1: none
   uint32_t there;              // no list: bit i, tokens 16i .. 16i + 15 are there
 };
-
-constexpr float kMinNormal = 1.17549435e-38f;  // 2^-126
 
 // x / 16 / (page_size / 16) for x < 2^30: the page of a position.
 __device__ __forceinline__ int page_index(const AttnArgs& a, int pos) {
@@ -642,6 +654,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
 
     // the running maximum is kLift - base; lim is -infinity until the row has seen something
     float o[NT][8][4], base[NT][2], lim[NT][2], l[NT][2];
+    bool low = false;  // held kDrop lower
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -664,6 +677,27 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       const auto v_scales = [&](int h, int k) {
         return *reinterpret_cast<const uint32_t*>(st.v + scales[h] + k * kKvScaleBytes);
       };
+      if constexpr (!FAST) {
+        const uint32_t r = top_scale(lane < 16 ? v_scales(0, lane) : v_scales(1, lane - 16));
+        if (!low && __any_sync(0xffffffffu, r > kHugeScale)) {
+          low = true;
+          const float f = ex2(-kDrop);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              base[nt][i] -= kDrop;
+              lim[nt][i] -= kDrop;
+              l[nt][i] *= f;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[nt][d][i] *= f;
+                o[nt][d][i + 2] *= f;
+              }
+            }
+        }
+      }
+      const float lift = !FAST && low ? kLift - kDrop : kLift;
       // position of token k of the tile, -1 where none is
       const auto pos_at = [&](int k) { return LIST ? st.pos[at + k] : (there >> (k >> 4)) & 1u ? j0 + k : -1; };
       // ---- scores: S[token][row] = K q^T
@@ -702,8 +736,8 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           }
         }
       }
-      // ---- softmax weights in log2 units, times the value's size
-      float k_top[H][2], v_exp[H][2], v_inv[H][2];
+      // ---- softmax weights in log2 units
+      float k_top[H][2], v_exp[H][2];
       if constexpr (!FAST) {
 #pragma unroll
         for (int h = 0; h < H; ++h)
@@ -711,12 +745,11 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           for (int i = 0; i < 2; ++i) {
             const uint32_t w = k_scales(h, 8 * i + tk), r = top_scale(w);
             k_top[h][i] = has_nan(w) ? nan_f32() : e8m0_value(r);
-            const uint32_t rv = top_value_scale(v_scales(h, 8 * i + tk));
-            v_exp[h][i] = (float)((int)rv - 127);
-            v_inv[h][i] = rv < 254u ? __uint_as_float((254u - rv) << 23) : 0.5f * kMinNormal;
+            v_exp[h][i] = (float)((int)top_scale(v_scales(h, 8 * i + tk)) - 127);
           }
       }
       uint32_t pf[H][NT][P][2];
+      float grow[NT][2];  // general form: the factor of a row's products
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         // x: log2 of the weights, relative to the running maximum and times 2^kLift.  [half][c]: tokens tk, tk,
@@ -753,12 +786,6 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
               x[h][c] += base[nt][c & 1];
             }
         }
-        if constexpr (!FAST) {
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[h][c] += v_exp[h][c >> 1];
-        }
         if constexpr (!WHOLE) {
 #pragma unroll
           for (int h = 0; h < H; ++h)
@@ -780,10 +807,10 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
             if (top > lim[nt][i]) {
-              const float down = top - kLift;
+              const float down = top - lift;
               const float f = lim[nt][i] == -INFINITY ? 0.f : ex2(-down);  // a row's first: there is nothing to rescale
               base[nt][i] -= down;
-              lim[nt][i] = kLift + kLazy;
+              lim[nt][i] = lift + kLazy;
 #pragma unroll
               for (int h = 0; h < H; ++h) {
                 x[h][i] -= down;
@@ -798,13 +825,36 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
             }
           }
         }
+        if constexpr (!FAST) {  // the sum, then the weights times sizes, relative to their largest in the tile
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              l[nt][c & 1] += ex2(x[h][c]);
+              x[h][c] += v_exp[h][c >> 1];
+            }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = fmaxf(fmaxf(x[0][i], x[0][i + 2]), fmaxf(x[1][i], x[1][i + 2]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float up = fmaxf(top - kLift, -120.f);  // a row that sees nothing here: its weights are 0 all the same
+            grow[nt][i] = ex2(up);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              x[h][i] -= up;
+              x[h][i + 2] -= up;
+            }
+          }
+        }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             w[c] = ex2(x[h][c]);
-            l[nt][c & 1] = FAST ? l[nt][c & 1] + w[c] : fmaf(w[c], v_inv[h][c >> 1], l[nt][c & 1]);
+            if constexpr (FAST) l[nt][c & 1] += w[c];
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -834,40 +884,84 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
         }
       }
       // ---- outputs: O[dim][row] += V^T P^T
+      if constexpr (FAST) {
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        uint32_t f[2];  // factors of tokens (t, t + 4) and (t + 8, t + 12) for dims 16g ..
-        uint2 vr[4];
+        for (int h = 0; h < H; ++h) {
+          uint32_t f[2];  // factors of tokens (t, t + 4) and (t + 8, t + 12) for dims 16g ..
+          uint2 vr[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vr[i] = *reinterpret_cast<const uint2*>(st.v + codes[h] + (4 * i + t) * kKvCodeBytes + 8 * g);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t wa = v_scales(h, 8 * i + t), wb = v_scales(h, 8 * i + 4 + t);
-          if constexpr (FAST) {
-            f[i] = fast_factor(__byte_perm(wa, wb, 0x4400 + 0x1111 * grp) & 0x00ff00ffu);
-          } else {
-            const uint32_t fa = byte_of(wa, grp) == 255u ? 0u : group_factor(wa, grp, top_value_scale(wa));
-            const uint32_t fb = byte_of(wb, grp) == 255u ? 0u : group_factor(wb, grp, top_value_scale(wb));
-            f[i] = fa | (fb << 16);
-          }
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // dims 16g .. +7, then +8 .. +15
-          uint32_t ev[2][4], od[2][4];
+          for (int i = 0; i < 4; ++i) vr[i] = *reinterpret_cast<const uint2*>(st.v + codes[h] + (4 * i + t) * kKvCodeBytes + 8 * g);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t wa = half ? vr[2 * i].y : vr[2 * i].x, wb = half ? vr[2 * i + 1].y : vr[2 * i + 1].x;
-            e2m1x8_to_f16((wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u), ev[i]);
-            e2m1x8_to_f16(((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u), od[i]);
+            const uint32_t wa = v_scales(h, 8 * i + t), wb = v_scales(h, 8 * i + 4 + t);
+            f[i] = fast_factor(__byte_perm(wa, wb, 0x4400 + 0x1111 * grp) & 0x00ff00ffu);
           }
 #pragma unroll
+          for (int half = 0; half < 2; ++half) {  // dims 16g .. +7, then +8 .. +15
+            uint32_t ev[2][4], od[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t wa = half ? vr[2 * i].y : vr[2 * i].x, wb = half ? vr[2 * i + 1].y : vr[2 * i + 1].x;
+              e2m1x8_to_f16((wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u), ev[i]);
+              e2m1x8_to_f16(((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u), od[i]);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t A[4] = {hmul2(ev[0][m], f[0]), hmul2(od[0][m], f[0]), hmul2(ev[1][m], f[1]),
+                                     hmul2(od[1][m], f[1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int p = 0; p < P; ++p) mma_f16(o[nt][4 * half + m], A, pf[h][nt][p][0], pf[h][nt][p][1]);
+            }
+          }
+        }
+      } else {
+        uint32_t f[H][2];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t wa = v_scales(h, 8 * i + t), wb = v_scales(h, 8 * i + 4 + t);
+            const uint32_t fa = byte_of(wa, grp) == 255u ? 0u : group_factor(wa, grp, top_scale(wa));
+            const uint32_t fb = byte_of(wb, grp) == 255u ? 0u : group_factor(wb, grp, top_scale(wb));
+            f[h][i] = fa | (fb << 16);
+          }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t ev[H][2], od[H][2];
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint8_t* at = st.v + codes[h] + (8 * i + t) * kKvCodeBytes + 8 * g + 4 * half;
+              const uint32_t wa = *reinterpret_cast<const uint32_t*>(at);
+              const uint32_t wb = *reinterpret_cast<const uint32_t*>(at + 4 * kKvCodeBytes);
+              ev[h][i] = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
+              od[h][i] = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
+            }
+#pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const uint32_t A[4] = {hmul2(ev[0][m], f[0]), hmul2(od[0][m], f[0]), hmul2(ev[1][m], f[1]),
-                                   hmul2(od[1][m], f[1])};
+            float acc[NT][4];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const uint32_t A[4] = {hmul2(e2m1x2_to_f16(ev[h][0] >> (8 * m)), f[h][0]),
+                                     hmul2(e2m1x2_to_f16(od[h][0] >> (8 * m)), f[h][0]),
+                                     hmul2(e2m1x2_to_f16(ev[h][1] >> (8 * m)), f[h][1]),
+                                     hmul2(e2m1x2_to_f16(od[h][1] >> (8 * m)), f[h][1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                  if (h == 0 && p == 0) mma_f16_zero(acc[nt], A, pf[h][nt][p][0], pf[h][nt][p][1]);
+                  else mma_f16(acc[nt], A, pf[h][nt][p][0], pf[h][nt][p][1]);
+                }
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int p = 0; p < P; ++p) mma_f16(o[nt][4 * half + m], A, pf[h][nt][p][0], pf[h][nt][p][1]);
+              for (int c = 0; c < 4; ++c)
+                o[nt][4 * half + m][c] = fmaf(acc[nt][c], grow[nt][c & 1], o[nt][4 * half + m][c]);
           }
         }
       }
@@ -888,7 +982,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
         const uint32_t there = LIST ? 0u : st.there >> (first * H);
         uint32_t kw[kMost], vw[kMost];  // the scales of this lane's token in each tile
         int at[kMost];
-        bool clear = true;  // seen whole, and with fast scales
+        bool clear = !low;  // seen whole, and with fast scales
 #pragma unroll
         for (int i = 0; i < kMost; ++i) {
           const int tile_i = i < n ? first + i : first;
@@ -922,7 +1016,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
               *reinterpret_cast<uint32_t*>(st.k + (i ? at[last] : at[0])) = 0x7f7f7f7fu;
               *reinterpret_cast<uint32_t*>(st.v + (i ? at[last] : at[0])) = 0x7f7f7f7fu;
             }
-            const bool fast = __all_sync(0xffffffffu, !seen || fast_scales(i ? kw[last] : kw[0], i ? vw[last] : vw[0]));
+            const bool fast = !low && __all_sync(0xffffffffu, !seen || fast_scales(i ? kw[last] : kw[0], i ? vw[last] : vw[0]));
             const bool whole = __all_sync(0xffffffffu, j >= lo_last && j <= p_first);
             const bool any = __any_sync(0xffffffffu, seen);
             __syncwarp();

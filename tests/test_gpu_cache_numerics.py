@@ -1,0 +1,117 @@
+"""The attention over the 4-bit cache where numbers are far apart: values of any
+size beside one another and beside records of zeros, capped scores, scores far
+below zero, and queries at the ends of their type.  Against the oracle in 64
+bits, with the tolerances of test_gpu_cache.py unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache as OC
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from learned_kv_chunk_b200 import fm  # noqa: E402  (loads libfm.so; raises if missing)
+from tests.test_gpu_cache import DEV, TYPES, check_attention, dev  # noqa: E402
+
+PAGE = 16
+
+
+def pages_of(x):
+    """[B, heads, n, 128] fp64 -> (pages, table): the records of the values (n a multiple of a page)."""
+    B, H, n, _ = x.shape
+    codes, scales = OC.quant4(x)
+    per = n // PAGE
+    blk = np.concatenate([codes.reshape(B, H, per, PAGE * 64), scales.reshape(B, H, per, PAGE * 4)], axis=-1)
+    return (np.ascontiguousarray(blk.transpose(0, 2, 1, 3)).reshape(B * per, H, PAGE * 68),
+            np.arange(B * per, dtype=np.int32).reshape(B, per))
+
+
+def check(q, k, v, lens, **kw):
+    """q [B, Tq, Hq, 128] torch, k and v [B, heads, n, 128] fp64, held as their records."""
+    kp, table = pages_of(k)
+    vp, _ = pages_of(v)
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.asarray(lens, np.int32)), **kw)
+    check_attention(o, q, kp, vp, table, lens, PAGE, **kw)
+
+
+def queries(rng, dtype, B=1, Tq=1, Hq=8, spread=1.0):
+    return torch.from_numpy(spread * rng.standard_normal((B, Tq, Hq, 128))).to(TYPES[dtype])
+
+
+# --------------------------------------------------- values of any size
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("Hq", [4, 12])
+def test_every_token_counts_in_the_sum_whatever_its_size(dtype, Hq):
+    """Two tokens of one score, 2^100 and 2^-40: each has half of the weight."""
+    rng = np.random.default_rng(1)
+    for big, small in ((100, -40), (125, -126), (60, -100)):
+        for order in (0, 1):
+            k, v = np.zeros((1, 1, 16, 128)), np.zeros((1, 1, 16, 128))
+            v[0, 0, order] = 2.0 ** big * rng.choice([1.0, 3.0, 6.0], 128)
+            v[0, 0, 1 - order] = 2.0 ** small
+            q = queries(rng, dtype, Hq=Hq)
+            check(q, k, v, [2])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("Hq,n", [(4, 3200), (12, 400), (12, 3200)])
+def test_a_huge_value_leaves_the_weights_of_ordinary_ones(dtype, Hq, n):
+    """One token of 6 * 2^125 some units above the others, whose weights of 2^-10 each add up to as much as its own."""
+    rng = np.random.default_rng(2)
+    k, v = np.zeros((1, 1, n, 128)), rng.standard_normal((1, 1, n, 128))
+    for at in (0, n // 2, n - 1):
+        k[0, 0] = 0.0
+        k[0, 0, at, 0] = 6.0
+        w = v.copy()
+        w[0, 0, at] = 6.0 * 2.0 ** 125
+        q = torch.zeros(1, 1, Hq, 128, dtype=TYPES[dtype])
+        q[..., 0] = torch.linspace(8.0, 14.0, Hq)  # scores of 4.2 to 7.4
+        check(q, k, w, [n])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_values_at_the_ends_of_the_scales(dtype):
+    """Thousands of tokens of 2^-126 or of 6 * 2^125: neither their sum nor their weights' leaves the range."""
+    rng = np.random.default_rng(3)
+    for size in (2.0 ** -124, 2.0 ** -110, 2.0 ** 110, 2.0 ** 125):
+        n = 9600
+        k = np.zeros((1, 1, n, 128))
+        v = size * rng.choice([1.0, 2.0, 6.0], (1, 1, n, 128))
+        q = queries(rng, dtype)
+        check(q, k, v, [n])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("Hq,Tq", [(4, 1), (12, 1), (6, 3)])
+@pytest.mark.parametrize("size", [0, -15, -30, -60])
+def test_records_of_zeros_among_small_values(dtype, Hq, Tq, size):
+    """A value of zeros takes its weight and nothing else: the others keep their accuracy."""
+    if dtype == "fp16" and size < -15:
+        pytest.skip("below fp16's numbers")
+    rng = np.random.default_rng(4)
+    n = 320
+    k = rng.standard_normal((1, 2, n, 128))
+    v = 2.0 ** size * rng.standard_normal((1, 2, n, 128))
+    for zeros in (np.arange(n) % 3 == 1, np.arange(n) == 5, np.arange(n) >= 7):
+        w = np.where(zeros[None, None, :, None], 0.0, v)
+        q = queries(rng, dtype, Tq=Tq, Hq=2 * Hq)
+        check(q, k, w, [n])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_sizes_mixed_at_random(dtype):
+    rng = np.random.default_rng(5)
+    n = 2000
+    for lo, hi in ((-120, 120), (-40, 40), (-20, 0)):
+        k = rng.standard_normal((2, 2, n, 128))
+        v = rng.standard_normal((2, 2, n, 128)) * np.exp2(rng.integers(lo, hi, (2, 2, n, 1)))
+        v[:, :, rng.random(n) < 0.1] = 0.0
+        v[:, :, 700:1200] = rng.standard_normal((2, 2, 500, 128))  # whole tiles of ordinary ones
+        for Hq in (6, 24):
+            q = queries(rng, dtype, B=2, Hq=Hq)
+            check(q, k, v, [n, n - 3])
