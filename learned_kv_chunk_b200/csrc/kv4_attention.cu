@@ -157,9 +157,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // cap * tanh(y) in log2 units = cap - 2 cap / (1 + e^2y), within 2^-22 cap: up to
-// kFarCap 2^-16 of a logit, what 16-bit queries lose anyway.  Above it small y go by the
-// series of tanh (its next term is below 2^-26 y for |y| < 1/4); the test for that
-// costs 3 % (32 rows of up to 8192 tokens with a cap: 53.2 us, 51.5 without).
+// kFarCap 2^-16 of a logit, a thirty-second of what the f16 weights of 16-bit calls lose.  Above
+// it small y go by the series of tanh (its next term is below 2^-26 y for |y| < 1/4); the
+// test for that costs 3 % (32 rows of up to 8192 tokens with a cap: 53.2 us, 51.5 without).
+// fp32 calls take tanhf, within two units of the result at every cap (32 rows in fp32: 62.5 us,
+// 61.3 by the difference).
 constexpr float kFarCap = 64.f;
 __device__ __forceinline__ float capped(const AttnArgs& a, float y) {
   return a.cap_log2 - __fdividef(2.f * a.cap_log2, 1.f + ex2(y * (2.f * kLog2e)));
@@ -773,8 +775,12 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const float y = x[h][c];
-                x[h][c] = capped(a, y);
-                if (a.softcap > kFarCap && fabsf(y) < 0.25f) x[h][c] = a.cap_log2 * tanh_near(y);
+                if constexpr (P == 2) {  // fp32
+                  x[h][c] = a.cap_log2 * tanhf(y);
+                } else {
+                  x[h][c] = capped(a, y);
+                  if (a.softcap > kFarCap && fabsf(y) < 0.25f) x[h][c] = a.cap_log2 * tanh_near(y);
+                }
               }
           }
 #pragma unroll

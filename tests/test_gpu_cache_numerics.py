@@ -14,7 +14,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 from learned_kv_chunk_b200 import fm  # noqa: E402  (loads libfm.so; raises if missing)
-from tests.test_gpu_cache import DEV, TYPES, check_attention, dev  # noqa: E402
+from tests.test_gpu_cache import DEV, TYPES, check_attention, dev, make_cache  # noqa: E402
 
 PAGE = 16
 
@@ -115,3 +115,56 @@ def test_sizes_mixed_at_random(dtype):
         for Hq in (6, 24):
             q = queries(rng, dtype, B=2, Hq=Hq)
             check(q, k, v, [n, n - 3])
+
+
+# -------------------------------------------------------- capped scores
+
+
+@pytest.mark.parametrize("softcap", [0.5, 2.0, 20.0, 30.0, 50.0, 64.0, 300.0])
+@pytest.mark.parametrize("G", [8, 16])
+@pytest.mark.parametrize("general", [False, True])
+def test_capped_scores_of_fp32_queries_are_those_of_fp32(softcap, G, general):
+    """Two tokens, scores x and 0 (|x| <= 1), values 1 and -1: out = tanh(capped(x) / 2).
+
+    An error dx of a logit moves out by at most dx / 2.  dx: the query's two
+    pieces 2^-23 |x|, four products and constants 2^-24 |x| each, tanhf two units
+    (2^-22 |x|), together below 2^-20 |x|; and the running maximum taken off and
+    its base added, which are held near 8: 2^-21 in log2 units, 0.7 of that in x,
+    twice for either token, below 2^-19.5.  The weights: exp2 to 2^-22 of either,
+    two pieces to 2^-23 of either, a quotient: 2.5 * 2^-22.  No term has the cap."""
+    rng = np.random.default_rng(6)
+    B, Hkv = 8, 8
+    x = rng.uniform(-1, 1, (B, Hkv * G)).astype(np.float32)
+    q = torch.zeros(B, 1, Hkv * G, 128)
+    q[:, 0, :, 0] = torch.from_numpy(x)
+    kp, vp = (np.zeros((1, Hkv, PAGE * 68), np.uint8) for _ in range(2))
+    for p in (kp, vp):
+        p[:, :, PAGE * 64:] = 127
+    if general:
+        kp[:, :, PAGE * 64 + 3] = 0  # a group of zeros of the first key
+    kp[:, :, 0] = 2               # the first key: 1 in its first dim
+    vp[:, :, :64], vp[:, :, 64:128] = 0x22, 0xaa
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(np.zeros((B, 1), np.int32)),
+                            dev(np.full(B, 2, np.int32)), scale=1.0, softcap=softcap)
+    x = x.astype(np.float64)
+    want = np.tanh(softcap * np.tanh(x / softcap) / 2)[:, None, :, None]
+    tol = 0.5 * (2.0 ** -20 * np.abs(x) + 2.0 ** -19.5) + 2.5 * 2.0 ** -22
+    off = np.abs(o.double().cpu().numpy() - want)
+    assert (off <= tol[:, None, :, None]).all(), off.max()
+
+
+@pytest.mark.parametrize("softcap", [1.0, 5.0, 20.0, 50.0])
+def test_caps_cost_fp32_calls_no_accuracy(softcap):
+    """Scores from a few units to far past the cap, every shape of the call: the tolerance has no term of the cap."""
+    rng = np.random.default_rng(7)
+    lens = [300, 41, 700]
+    for spread, Hq in ((0.05, 8), (0.5, 24), (3.0, 8)):
+        kp, vp, table = make_cache(rng, lens, 2, PAGE)
+        q = torch.from_numpy(spread * rng.standard_normal((3, 2, Hq, 128))).float()
+        o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.asarray(lens, np.int32)), softcap=softcap)
+        k, there = OC.read_cache(kp, table, PAGE)
+        v, _ = OC.read_cache(vp, table, PAGE)
+        ref, _, abs_v, top_v = OC.attention(q.double().numpy(), k, v, there, lens, softcap=softcap)
+        _, err_x, _, _ = OC.attention(q.double().numpy(), k, v, there, lens)
+        tol = (2 * 2.0 ** -20 * err_x + 2.0 ** -20 + 2.0 ** -23 * (700 / 16 + 16)) * abs_v + top_v + 2.0 ** -24 * np.abs(ref) + 1e-37
+        assert (np.abs(o.double().cpu().numpy() - ref) <= tol).all()
