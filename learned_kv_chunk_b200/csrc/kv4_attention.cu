@@ -85,7 +85,7 @@ struct Shape {
 };
 constexpr int kCtas = 2;     // that an SM holds
 
-constexpr float kNoMax = -1e30f;          // the running maximum of a row that has seen nothing
+constexpr float kNoMax = -3.402823466e38f;  // the maximum of a row that has seen nothing: no number is below it
 constexpr float kLazy = 6.f;              // the maximum may be exceeded by 2^6 before the sums are rescaled
 constexpr float kLift = 8.f;              // weights are held times 2^8: at most 2^14 in f16
 // Where a value's scale passes 2^72 the outputs could leave fp32's range: from such a tile on a segment's sums are

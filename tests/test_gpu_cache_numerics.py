@@ -168,3 +168,30 @@ def test_caps_cost_fp32_calls_no_accuracy(softcap):
         _, err_x, _, _ = OC.attention(q.double().numpy(), k, v, there, lens)
         tol = (2 * 2.0 ** -20 * err_x + 2.0 ** -20 + 2.0 ** -23 * (700 / 16 + 16)) * abs_v + top_v + 2.0 ** -24 * np.abs(ref) + 1e-37
         assert (np.abs(o.double().cpu().numpy() - ref) <= tol).all()
+
+
+# ------------------------------------------------- scores far from zero
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("Hq,tokens", [(4, 60), (12, 60), (4, 3000), (12, 3000)])
+@pytest.mark.parametrize("slope", [1e20, 2e30, 1e34])
+def test_rows_whose_scores_are_all_far_below_zero(dtype, Hq, tokens, slope):
+    """A kept list without the newest tokens and a steep bias: the nearest kept token has the whole weight, in
+    whichever CTA or warp it is.  Its weight over itself is 1 within the f16 weights' 2^-11 (fp32: 2^-20)."""
+    rng = np.random.default_rng(8)
+    lens = [tokens, tokens - 1]
+    kp, vp, table = make_cache(rng, lens, 1, PAGE, hi=128)
+    near = [tokens // 2, 7]
+    idx = np.stack([np.r_[np.arange(n), n, np.full(tokens - n - 1, -1)] for n in near])
+    order = rng.permutation(tokens)
+    count = np.full(2, tokens)
+    q = torch.from_numpy(rng.standard_normal((2, Hq, 128))).to(TYPES[dtype])
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.asarray(lens, np.int32)),
+                            slopes=torch.full((Hq,), slope, device=DEV), idx=dev(idx[:, order].astype(np.int32)),
+                            count=dev(count.astype(np.int32)))
+    v, _ = OC.read_cache(vp, table, PAGE)
+    for b in range(2):
+        want = v[b, 0, near[b]]
+        tol = (2.0 ** -20 if dtype == "fp32" else 2.0 ** -11 + 2.0 ** -8) * np.abs(want)
+        assert (np.abs(o[b].double().cpu().numpy() - want) <= tol).all()
