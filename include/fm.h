@@ -571,7 +571,8 @@ typedef struct fm_kv4_attn_desc {
 } fm_kv4_attn_desc;
 
 /* Bytes of device workspace fm_kv4_attention needs (it depends on B, Tq, the
- * heads, max_len and max_sel only); 0 for a descriptor that it would refuse. */
+ * heads, max_len and max_sel only: one does for every window, with idx or
+ * without); 0 for a descriptor that it would refuse. */
 size_t fm_kv4_attention_workspace_bytes(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d);
 
 /* ws: caller-owned, 16-byte aligned; contents on entry irrelevant.  Calls that

@@ -1208,14 +1208,12 @@ struct AttnPlan {
 constexpr int kSms = 148;
 constexpr int kWholeBlocks = 4;
 
-AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
+// For rows of up to `tokens` tokens (list entries) each.
+AttnPlan plan_for(const fm_kv4_cache* c, const fm_kv4_attn_desc* d, int64_t tokens) {
   AttnPlan p;
   const int rows = d->Tq * (d->n_q_heads / c->n_kv_heads);
   p.nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
-  int64_t tokens = d->idx ? d->max_sel : d->max_len;
-  if (!d->idx && d->window > 0)  // a row reaches back window + Tq - 1 from the last token, from a multiple of 128
-    tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kBlock - 1);
   const int64_t units = (int64_t)c->B * c->n_kv_heads * p.row_tiles;
   // Up to 512 tokens a CTA does a whole unit, which saves the merge and its launch (one row of 500 tokens and 8 kv
   // heads: 12.1 us, shared out 12.4; of 1001 tokens: 14.5 and 12.4).
@@ -1224,6 +1222,13 @@ AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   p.grid = (int)std::min<int64_t>(p.whole ? units : units * blocks, kSms * kCtas);
   p.wide = 8 * units <= p.grid;
   return p;
+}
+
+AttnPlan plan_of(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
+  int64_t tokens = d->idx ? d->max_sel : d->max_len;
+  if (!d->idx && d->window > 0)  // a row reaches back window + Tq - 1 from the last token, from a multiple of 128
+    tokens = std::min(tokens, (int64_t)d->window + d->Tq - 1 + kBlock - 1);
+  return plan_for(c, d, tokens);
 }
 
 // Bytes of the workspace's parts.
@@ -1275,7 +1280,8 @@ using namespace fm;
 
 extern "C" size_t fm_kv4_attention_workspace_bytes(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   if (check_attn(c, d) != FM_OK) return 0;
-  return space_of(plan_of(c, d)).total();
+  // of the longest call with these sizes, whatever its window, with a list or without: space grows with the tokens
+  return space_of(plan_for(c, d, std::max(d->max_len, d->max_sel))).total();
 }
 
 namespace {

@@ -265,3 +265,22 @@ def test_oracle_attention_reduces_to_plain_cases():
     o, *_ = OC.attention(np.zeros((1, 3, 1, 128)), k, v, there, [2])
     assert not o[0, 0].any()  # the first of three queries stands before the row's start
     np.testing.assert_allclose(o[0, 1, 0], v[0, 0, 0])
+
+
+@pytest.mark.parametrize("max_len,max_sel,kw", [
+    (16384, 0, {}), (16384, 4096, {}), (300, 0, {}), (300, 4096, {}), (16384, 100, dict(Tq=4)),
+    (16384, 16384, dict(n_q_heads=128))])
+def test_one_workspace_does_for_every_window_and_list_of_the_same_sizes(max_len, max_sel, kw):
+    """Sized once from B, Tq, the heads, max_len and max_sel: a sliding-window layer's buffer also does for a layer
+    without a window, and with or without a list (each at the sizes that it was asked for)."""
+    c = cache(max_pages=1024, page_table_stride=1024)
+    size = fm.lib().fm_kv4_attention_workspace_bytes
+    need = set()
+    for window in (0, 1, 128, 385, 4096, 1 << 30):
+        for listed in ([False, True] if max_sel else [False]):
+            d = attn_desc(max_len=max_len, max_sel=max_sel, window=window, idx=FAKE if listed else None,
+                          count=FAKE if listed else None, **kw)
+            need.add(size(ctypes.byref(c), ctypes.byref(d)))
+            # one byte less is refused (before anything is launched)
+            assert fm.lib().fm_kv4_attention(ctypes.byref(c), ctypes.byref(d), FAKE, max(need) - 1, None) == INVALID
+    assert len(need) == 1 and need.pop() > 0
