@@ -556,7 +556,8 @@ typedef struct fm_kv4_attn_desc {
   int n_q_heads;              /* a multiple of n_kv_heads, at most 1024 */
   const void* q;              /* [B, Tq, n_q_heads, 128] device, 16-byte aligned, heads packed */
   int64_t q_stride;           /* elements between tokens (b, t) -> (b, t + 1) -> ...: a multiple of 16 bytes */
-  void* out;                  /* [B, Tq, n_q_heads, 128] device, 16-byte aligned, packed (written) */
+  void* out;                  /* [B, Tq, n_q_heads, 128] device, 16-byte aligned, packed (written); may be q when that is
+                                 packed */
   const int32_t* kv_len;      /* [B] device: cached tokens of a row, clamped to [0, max_len] */
   const int32_t* kv_start;    /* [B] device or NULL: the first visible position (a document's start, left padding) */
   int max_len;                /* a bound of kv_len, 1..max_pages * page_size: sizes the launch */

@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_rmsnorm_kernel(cons
     if (a.sum_out) store8(static_cast<T*>(a.sum_out) + row * a.H + 8 * i, z[v]);
     if (a.gain) {
       float w[8];
-      load8(gain + 8 * i, w);
+      ldg8(gain + 8 * i, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) z[v][k] *= w[k];
     }

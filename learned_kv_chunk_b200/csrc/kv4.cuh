@@ -50,8 +50,17 @@ template <class T>
 struct Raw8 {
   uint4 w[sizeof(T) / 2];
 };
+// (an ordinary load: right for operands that the kernel also writes, such as queries rotated in place)
 template <class T>
 __device__ __forceinline__ Raw8<T> load_raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+// The same through the read-only path: for what no thread of the kernel writes.
+template <class T>
+__device__ __forceinline__ Raw8<T> ldg_raw8(const T* p) {
   Raw8<T> r;
 #pragma unroll
   for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
@@ -86,6 +95,10 @@ __device__ __forceinline__ void to_f32(const Raw8<__half>& r, float (&v)[8]) {
 template <class T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
   to_f32(load_raw8(p), v);
+}
+template <class T>
+__device__ __forceinline__ void ldg8(const T* p, float (&v)[8]) {
+  to_f32(ldg_raw8(p), v);
 }
 
 // Eight fp32 values rounded to the type and stored (p 16-byte aligned).

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexAr
   int layer = w - tok * a.spread;
   const T* src = static_cast<const T*>(a.k) + t * a.stride + 8 * l;
   Raw8<T> ahead = {};
-  if (in) ahead = load_raw8(src + layer * kKvDim);
+  if (in) ahead = ldg_raw8(src + layer * kKvDim);
   const int row = in ? __ldg(a.row + t) : -1, chunk = in ? __ldg(a.chunk + t) : -1;
   const bool on = row >= 0 && row < a.B && chunk >= 0 && chunk < a.N;
   if (RD) {
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kAppThreads) index_append_kernel(const IndexAr
   for (int i = 0; i < a.L; i += a.spread, layer += a.spread) {
     float x[8];
     to_f32(ahead, x);
-    if (in && layer + a.spread < a.L) ahead = load_raw8(src + (layer + a.spread) * kKvDim);
+    if (in && layer + a.spread < a.L) ahead = ldg_raw8(src + (layer + a.spread) * kKvDim);
     rotate8<RD, kRotNear>(x, l, turn);
     if (a.hadamard) {
 #pragma unroll

@@ -780,3 +780,57 @@ def test_a_decode_step_from_the_hidden_state_to_the_output():
             assert (np.abs(o.double().cpu().numpy()[:, None] - ref) <= tol).all()
     finally:
         r.close()
+
+
+# ------------------------------------------------------------------ in place
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,H", [(9, 128), (5, 512), (300, 1024), (33, 2048), (17, 4096), (5, 8192), (3, 16384), (2, 32768)])
+def test_norm_into_its_operands_is_the_norm(dtype, T, H):
+    """Every width of row, the sum written over x or over the residual."""
+    rng = np.random.default_rng(H)
+    x, r = (torch.from_numpy(rng.standard_normal((T, H))).to(TYPES[dtype]).to(DEV) for _ in range(2))
+    g = torch.from_numpy(1 + 0.1 * rng.standard_normal(H)).to(TYPES[dtype]).to(DEV)
+    for group in (128, H):
+        want = fm.fm_add_rmsnorm_fp8(x, r, g, group=group)
+        for which in (0, 1):
+            ops = [x.clone(), r.clone()]
+            got = fm.fm_add_rmsnorm_fp8(*ops, g, group=group, sum_out=ops[which])
+            assert got[0].data_ptr() == ops[which].data_ptr()
+            for a, b in zip(want, got):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,Hq,Hkv,rope_dim", [(1, 3, 1, 64), (64, 64, 8, 64), (40, 5, 2, 128), (3000, 32, 8, 128)])
+def test_queries_rotated_in_place_are_the_rotated_queries(dtype, T, Hq, Hkv, rope_dim):
+    rng = np.random.default_rng(T)
+    qkv = torch.from_numpy(rng.standard_normal((T, Hq + 2 * Hkv, 128))).to(TYPES[dtype]).to(DEV)
+    pages = torch.zeros(T // 16 + 1, Hkv, 16 * 68, device=DEV, dtype=torch.uint8)
+    table = torch.arange(T // 16 + 1, device=DEV, dtype=torch.int32).view(1, -1)
+    seq, pos = torch.zeros(T, device=DEV, dtype=torch.int32), torch.arange(T, device=DEV)
+    freq = dev(O.yarn_inv_freq(rope_dim=rope_dim))
+    outs = []
+    for in_place in (False, True):
+        g, kp, vp = qkv.clone(), pages.clone(), pages.clone()
+        q = g[:, :Hq]
+        o, _, _ = fm.fm_kv4_append(g[:, Hq:Hq + Hkv], g[:, Hq + Hkv:], kp, vp, table, seq, pos, inv_freq=freq, q=q,
+                                   q_out=q if in_place else None)
+        outs.append((o.clone(), kp, vp))
+        assert torch.equal(g[:, Hq:], qkv[:, Hq:])
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("lens,Hq,Hkv,Tq", [([300, 20, 0], 8, 2, 1), ([5000, 4000, 17], 8, 2, 1), ([5000, 4000, 17], 24, 2, 3)])
+def test_attention_into_its_queries_is_the_attention(dtype, lens, Hq, Hkv, Tq):
+    rng = np.random.default_rng(51)
+    kp, vp, table = (dev(x) for x in make_cache(rng, lens, Hkv, 16))
+    q = torch.from_numpy(rng.standard_normal((len(lens), Tq, Hq, 128))).to(TYPES[dtype]).to(DEV)
+    n = dev(np.asarray(lens, np.int32))
+    want = fm.fm_kv4_attention(q, kp, vp, table, n)
+    got = q.clone()
+    fm.fm_kv4_attention(got, kp, vp, table, n, out=got)
+    assert torch.equal(want, got)
