@@ -218,6 +218,12 @@ __device__ __forceinline__ uint32_t top_scale(uint32_t w) {
   for (int i = 0; i < 4; ++i) r = max(r, byte_of(w, i) == 255u ? 0u : byte_of(w, i));
   return r;
 }
+// The factor of a score, held within fp32's numbers: a query and a key that give 0 have a score of 0, however
+// large the scale, the query and the key's scales are (a NaN stays).
+__device__ __forceinline__ float bounded(float x) {
+  constexpr float kMost = 3.402823466e38f;
+  return x > kMost ? kMost : x < -kMost ? -kMost : x;
+}
 // f16 bits of 2^(byte i - r), 0 below 2^-25.
 __device__ __forceinline__ uint32_t group_factor(uint32_t w, int i, uint32_t r) {
   const __half h = __float2half_rn(__int_as_float(max(127 + (int)byte_of(w, i) - (int)r, 0) << 23));
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int e = max(-110, min(120, (int)(__float_as_uint(m) >> 23) - 127 - 7));  // m * 2^-e in [2^7, 2^8)
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      const float c = a.coef * __uint_as_float((uint32_t)(127 + e) << 23);
+      const float c = bounded(a.coef * __uint_as_float((uint32_t)(127 + e) << 23));
       if constexpr (kQReg) {
         coef[0][0] = __shfl_sync(0xffffffffu, c, 8 * t);
         coef[0][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
@@ -754,6 +760,9 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       float grow[NT][2];  // general form: the factor of a row's products
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        const auto k_coef = [&](int h, int c) {  // what a score is multiplied by
+          return FAST ? coef[nt][c & 1] : bounded(coef[nt][c & 1] * k_top[h][c >> 1]);
+        };
         // x: log2 of the weights, relative to the running maximum and times 2^kLift.  [half][c]: tokens tk, tk,
         // tk + 8, tk + 8; columns 2t, 2t + 1, 2t, 2t + 1
         float x[H][4];
@@ -762,13 +771,13 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              x[h][c] = fmaf(s[h][nt][c], FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1], base[nt][c & 1]);
+              x[h][c] = fmaf(s[h][nt][c], k_coef(h, c), base[nt][c & 1]);
         } else {
 #pragma unroll
           for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              x[h][c] = s[h][nt][c] * (FAST ? coef[nt][c & 1] : coef[nt][c & 1] * k_top[h][c >> 1]);
+              x[h][c] = s[h][nt][c] * k_coef(h, c);
           if (a.softcap > 0.f) {  // coef holds scale / softcap
 #pragma unroll
             for (int h = 0; h < H; ++h)
@@ -1252,7 +1261,8 @@ fm_status check_attn(const fm_kv4_cache* c, const fm_kv4_attn_desc* d) {
   if (d->Tq > kMaxTq) return FM_ERR_UNSUPPORTED;
   if (d->max_len < 1 || d->max_len > (int64_t)c->max_pages * c->page_size) return FM_ERR_INVALID_ARG;
   if (d->idx && (!d->count || d->max_sel < 1 || d->max_sel > (1 << 30))) return FM_ERR_INVALID_ARG;
-  // within 2^32, and a cap not below 2^-32: then their quotient times a query's power of two is a number
+  // within 2^32, and a cap not below 2^-32: their quotient times a query's power of two is then a number for queries
+  // up to 2^70, and held to the largest one beyond (bounded)
   constexpr float kMost = 4294967296.f;
   if (!(std::fabs(d->scale) <= kMost) || d->window < 0) return FM_ERR_INVALID_ARG;
   if (d->softcap != 0.f && !(d->softcap >= 1.f / kMost && d->softcap <= kMost)) return FM_ERR_INVALID_ARG;

@@ -195,3 +195,27 @@ def test_rows_whose_scores_are_all_far_below_zero(dtype, Hq, tokens, slope):
         want = v[b, 0, near[b]]
         tol = (2.0 ** -20 if dtype == "fp32" else 2.0 ** -11 + 2.0 ** -8) * np.abs(want)
         assert (np.abs(o[b].double().cpu().numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("Hq", [4, 12])
+@pytest.mark.parametrize("scale,softcap", [(2.0 ** 32, 2.0 ** -32), (-2.0 ** 32, 2.0 ** -32), (2.0 ** 32, 0.0), (0.1, 0.0),
+                                           (1.0, 2.0 ** -32)])
+@pytest.mark.parametrize("key_scale", [0, 127, 252])
+def test_products_of_zero_stay_zero_whatever_multiplies_them(dtype, Hq, scale, softcap, key_scale):
+    """The largest queries against keys of zeros, or keys whose only elements meet zeros of the query: every score is
+    0, and the output the mean of the values."""
+    rng = np.random.default_rng(9)
+    n = 40
+    _, vp, table = make_cache(rng, [n], 1, PAGE)
+    kp = np.zeros_like(vp)
+    kp[:, :, PAGE * 64:] = key_scale
+    if key_scale:
+        kp[:, :, :PAGE * 64:64] = 0x70  # dim 1 of every key: 6
+    q = torch.zeros(1, 1, Hq, 128, dtype=TYPES[dtype])
+    q[..., 0] = torch.finfo(TYPES[dtype]).max
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.array([n], np.int32)), scale=scale, softcap=softcap)
+    v, _ = OC.read_cache(vp, table, PAGE)
+    want, size = v[0, 0, :n].mean(0), np.abs(v[0, 0, :n]).mean(0)
+    tol = (2.0 ** -18 if dtype == "fp32" else 2.0 ** -11 + 2.0 ** -8) * size
+    assert (np.abs(o[0, 0].double().cpu().numpy() - want) <= tol).all()
