@@ -546,10 +546,21 @@ fm_status fm_kv4_append(const fm_kv4_cache* cache, const fm_kv4_append_desc* d, 
  * A query that sees nothing gives 0 (kv_len 0, a position below 0, an empty
  * window or list).  What a query does not see is not touched by it, whatever
  * its records hold.  Query head h uses kv head h / (n_q_heads / n_kv_heads).
- * Dot products, statistics and sums are fp32.  The products' operands are f16:
- * 16-bit queries enter exactly and their weights at 2^-11, fp32 queries and
- * their weights in two pieces at 2^-22; a weight below 2^-22 of the largest has
- * an absolute step of 2^-33 of that. */
+ * Dot products, statistics and sums are fp32.  The products' operands are f16,
+ * whose steps end at 2^-24; so each is also off by a part of its largest one:
+ *
+ *   queries  16-bit ones exact, fp32 ones in two pieces, to 2^-22 of an element;
+ *            and to 2^-32 of the head's largest element
+ *   weights  to 2^-11 (16-bit calls), 2^-22 (fp32) of a weight; and to 2^-33 of
+ *            the largest
+ *   keys,    exact where all scales of a tile of 32 tokens lie in 2^-14 .. 2^12;
+ *   values   in other tiles relative to each record's largest scale, to 2^-25 of
+ *            it, and a group whose scale is 2^-25 of it or less counts as zeros
+ *
+ * Scores, and the factor of a score (scale * 2^e for queries of size 2^e, over a
+ * cap, times a key's scale), count as infinite and as the largest float past
+ * fp32's range.  A cap is within 2^-22 of itself in 16-bit calls up to a cap of
+ * 64, and within two units of tanh beyond and in fp32. */
 typedef struct fm_kv4_attn_desc {
   int dtype;                  /* FM_F32, FM_BF16, FM_F16: of q and out */
   int Tq;                     /* query tokens of every row, 1..64 */

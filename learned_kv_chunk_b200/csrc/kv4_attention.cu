@@ -1,8 +1,11 @@
 // kv4_attention.cu -- attention over the 4-bit paged cache (fm_kv4_attention).
 //
-// Mathematics.  The codes go to the matrix instructions as f16: a code times its
-// group's scale is exact there, so only the queries (two pieces for fp32) and the
-// softmax weights are rounded.  S^T = K q^T and O^T = V^T P^T by m16n8k16, tokens
+// Mathematics.  The codes go to the matrix instructions as f16.  A code times its
+// group's scale is exact there within 2^-14 .. 2^12 (other tiles: relative to its
+// record's largest scale, to 2^-25 of that).  Queries are scaled to a largest
+// element of 2^7 and rounded (two pieces for fp32), softmax weights to 2^-11 (two
+// pieces: 2^-22): f16 halves what a weight moves through registers, and 16-bit
+// outputs lose as much or more.  S^T = K q^T and O^T = V^T P^T by m16n8k16, tokens
 // (then dimensions) in the 16 rows and query rows in the 8 columns, so 8 query
 // heads of a kv head fill an instruction and no row of it is padding.
 //   * A lane's 16 bytes of a key's codes are one scale group: the dimensions of a

@@ -219,3 +219,62 @@ def test_products_of_zero_stay_zero_whatever_multiplies_them(dtype, Hq, scale, s
     want, size = v[0, 0, :n].mean(0), np.abs(v[0, 0, :n]).mean(0)
     tol = (2.0 ** -18 if dtype == "fp32" else 2.0 ** -11 + 2.0 ** -8) * size
     assert (np.abs(o[0, 0].double().cpu().numpy() - want) <= tol).all()
+
+
+# --------------------------------------------- what the f16 operands cost
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("below", [8, 20, 24, 28, 32, 40])
+def test_query_elements_far_below_the_largest(dtype, G, below):
+    """The head's largest element meets zeros of the keys; the others are 2^-below of it and make the score.  A query
+    element is off by 2^-22 of itself (fp32; 16-bit ones by nothing) and 2^-32 of the head's largest."""
+    if dtype == "fp16" and below > 20:
+        pytest.skip("fp16 ends there")
+    rng = np.random.default_rng(below)
+    n, top = 64, 8.0
+    q = top * 2.0 ** -below * rng.uniform(0.5, 1, (1, 1, 2 * G, 128)) * rng.choice([-1, 1], (1, 1, 2 * G, 128))
+    q[..., 0] = top
+    q = torch.from_numpy(q).to(TYPES[dtype])
+    k = 2.0 ** (below - 6) * rng.uniform(0.5, 6, (1, 2, n, 128)) * rng.choice([-1, 1], (1, 2, n, 128))
+    k[..., 0] = 0.0
+    kp, table = pages_of(k)
+    vp, _ = pages_of(rng.standard_normal((1, 2, n, 128)))
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.array([n], np.int32)))
+    k, there = OC.read_cache(kp, table, PAGE)
+    v, _ = OC.read_cache(vp, table, PAGE)
+    ref, err_x, abs_v, top_v = OC.attention(q.double().numpy(), k, v, there, [n])
+    narrow = dtype != "fp32"
+    dx = 2.0 ** -32 * top * np.abs(k[0]).sum(-1).max() * 128 ** -0.5 + (0.0 if narrow else 2.0 ** -22) * err_x + 2.0 ** -20 * err_x
+    w = (2.0 ** -11 if narrow else 2.0 ** -20) + 2.0 ** -23 * 20
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    tol = (2 * dx + w) * abs_v + top_v + half * np.abs(ref) + 2.0 ** -25
+    assert (np.abs(o.double().cpu().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("below", [10, 16, 22, 24, 25, 26, 40, 126])
+def test_groups_far_below_their_record(dtype, below):
+    """Dims 96..127 of every key and value are 2^-below of the others: off by at most 2^-25 of the record's largest
+    scale where they are kept, or by themselves, at most 6 * 2^-25 of it, where they are not."""
+    rng = np.random.default_rng(below)
+    n, G = 64, 8
+    small = np.where(np.arange(128) < 96, 1.0, 2.0 ** -below)
+    q = torch.from_numpy(rng.standard_normal((1, 1, G, 128))).to(TYPES[dtype])
+    x = [rng.standard_normal((1, 1, n, 128)) * small for _ in range(2)]
+    x[1][..., 5, :] = 0.0  # (the tile takes the general form whatever the group's scale)
+    (kp, table), (vp, _) = pages_of(x[0]), pages_of(x[1])
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.array([n], np.int32)))
+    k, there = OC.read_cache(kp, table, PAGE)
+    v, _ = OC.read_cache(vp, table, PAGE)
+    ref, err_x, abs_v, top_v = OC.attention(q.double().numpy(), k, v, there, [n])
+    narrow = dtype != "fp32"
+    # a largest element is at least 3 of its scale, as it was quantised: 2^-25 and 6 * 2^-25 of the scale are at most 2^-24
+    # of the element
+    lost = 2.0 ** -24
+    dx = lost * np.abs(q.double().numpy()).sum(-1, keepdims=True) * np.abs(k).max() * 128 ** -0.5 + 2.0 ** -20 * err_x
+    w = (2.0 ** -11 if narrow else 2.0 ** -20) + 2.0 ** -23 * 20
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    tol = (2 * dx + w) * abs_v + lost * np.abs(v).max() + top_v + half * np.abs(ref)
+    assert (np.abs(o.double().cpu().numpy() - ref) <= tol).all()
