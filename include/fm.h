@@ -506,7 +506,9 @@ fm_status fm_rope_frequencies(const fm_config* cfg, double* inv_freq_host);
  * [0, B), pos[t] outside [0, max_pages * page_size) or a page that is not
  * there is padding: nothing is written for it, in the cache or in the
  * outputs.  Two tokens of one call must not name the same slot (the slot then
- * holds a mixture of the two).
+ * holds a mixture of the two).  The two pools must not overlap, nor the outputs
+ * one another or an input (q_out may be q); one pool for both, or one output, is
+ * FM_ERR_INVALID_ARG.
  *
  * Rotation: half-split pairs of the last rope_dim dimensions, as query prep
  * does it: x1' = x1 c - x2 s, x2' = x2 c + x1 s with c, s = fp32(cos, sin of
@@ -603,7 +605,9 @@ fm_status fm_kv4_attention(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d,
  * below 2^-126 is stored as zeros with scale 0; one with a NaN or an infinity
  * gets a NaN scale.  A token with row[t] outside [0, B) or chunk[t] outside
  * [0, N) is padding: nothing is written.  Two tokens of one call must not
- * name the same record.
+ * name the same record, and the layers' tensors must not overlap (the same
+ * pointer twice is FM_ERR_INVALID_ARG: append a key tensor that the layers share
+ * with L = 1).
  * k [T, L, 128] device, 16-byte aligned, token_stride elements between tokens
  * (times the element size: a multiple of 16); 1 <= T <= 2^30; 1 <= L <= 4; comp_k: array of L
  * device pointers (host array), 4-byte aligned, row b at + b *

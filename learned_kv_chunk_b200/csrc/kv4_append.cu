@@ -449,6 +449,8 @@ extern "C" fm_status fm_kv4_append(const fm_kv4_cache* c, const fm_kv4_append_de
       (reinterpret_cast<uintptr_t>(d->pos) & 7u) || (reinterpret_cast<uintptr_t>(d->positions) & 7u) ||
       (reinterpret_cast<uintptr_t>(d->inv_freq) & 7u))
     return FM_ERR_ALIGNMENT;
+  // keys and values written to one place
+  if (c->k_pages == c->v_pages || (d->k_hat && d->k_hat == d->v_hat)) return FM_ERR_INVALID_ARG;
   AppendArgs a = {};
   a.c = kv4_view(*c);
   a.x[0] = d->q; a.x[1] = d->k; a.x[2] = d->v;
@@ -501,6 +503,9 @@ extern "C" fm_status fm_index_append(const void* k, int dtype, int64_t token_str
     if (reinterpret_cast<uintptr_t>(comp_k[l]) & 3u) return FM_ERR_ALIGNMENT;
     a.comp_k[l] = comp_k[l];
   }
+  for (int l = 1; l < L; ++l)
+    for (int m = 0; m < l; ++m)
+      if (comp_k[l] == comp_k[m]) return FM_ERR_INVALID_ARG;  // two layers' records written to one place
   a.k = k;
   a.stride = token_stride;
   a.row = row;

@@ -284,3 +284,21 @@ def test_one_workspace_does_for_every_window_and_list_of_the_same_sizes(max_len,
             # one byte less is refused (before anything is launched)
             assert fm.lib().fm_kv4_attention(ctypes.byref(c), ctypes.byref(d), FAKE, max(need) - 1, None) == INVALID
     assert len(need) == 1 and need.pop() > 0
+
+
+def test_records_that_would_be_written_over_one_another_are_refused():
+    """Keys and values in one pool, or two layers' records in one tensor: the calls would write both to one place."""
+    one = cache()
+    other = cache(v_pages=FAKE + (1 << 20))
+    a = append_desc()
+    assert fm.lib().fm_kv4_append(ctypes.byref(one), ctypes.byref(a), None) == INVALID
+    a = append_desc(k_hat=FAKE, v_hat=FAKE)
+    assert fm.lib().fm_kv4_append(ctypes.byref(other), ctypes.byref(a), None) == INVALID
+    f = fm.lib().fm_index_append
+    for keys in ((FAKE, FAKE + 4096, FAKE), (FAKE, FAKE, FAKE + 4096)):
+        arr = (ctypes.c_void_p * 3)(*keys)
+        assert f(FAKE, 0, 384, 5, 3, FAKE, FAKE, FAKE, FAKE, 64, 1, arr, 132 * 8, 2, 8, None) == INVALID
+    # reading keys and values from one pool is the caller's choice
+    d = attn_desc()
+    size = fm.lib().fm_kv4_attention_workspace_bytes
+    assert size(ctypes.byref(one), ctypes.byref(d)) == size(ctypes.byref(other), ctypes.byref(d)) > 0
