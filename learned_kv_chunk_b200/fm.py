@@ -788,7 +788,7 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     if idx is not None:
         if idx.dim() != 2 or count is None:
             raise ValueError("idx must be int32 [B, max_sel], with count")
-        max_sel = idx.shape[1]
+        max_sel = _i32(idx.shape[1], "the entries of idx")
         _like(idx, (B, max_sel), torch.int32, "idx")
         _like(count, (B,), torch.int32, "count")
     elif count is not None:
@@ -839,7 +839,7 @@ def fm_index_append(k: torch.Tensor, comp_k: Sequence[torch.Tensor], row: torch.
         raise ValueError("positions and inv_freq belong together")
     if positions is not None:
         _like(positions, (T,), torch.int64, "positions")
-    N = N_pad if N is None else int(N)
+    N = N_pad if N is None else _i32(N, "N")
     if N > N_pad:
         raise ValueError("N exceeds the rows of comp_k")
     index, raw, _ = _where(stream, k, *comp_k, row, chunk, inv_freq, positions)

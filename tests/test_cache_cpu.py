@@ -302,3 +302,17 @@ def test_records_that_would_be_written_over_one_another_are_refused():
     d = attn_desc()
     size = fm.lib().fm_kv4_attention_workspace_bytes
     assert size(ctypes.byref(one), ctypes.byref(d)) == size(ctypes.byref(other), ctypes.byref(d)) > 0
+
+
+def test_a_list_longer_than_32_bits_is_refused():
+    """(Tensors without memory: the check comes before anything looks at their device.)"""
+    meta = dict(device="meta")
+    q = torch.empty(1, 1, 128, **meta)
+    pages, table = torch.empty(1, 1, 16 * 68, dtype=torch.uint8, **meta), torch.empty(1, 1, dtype=torch.int32, **meta)
+    one = torch.empty(1, dtype=torch.int32, **meta)
+    idx = torch.empty(1, (1 << 32) + 5, dtype=torch.int32, **meta)
+    with pytest.raises(ValueError, match="32 bits"):
+        fm.fm_kv4_attention(q, pages, pages, table, one, idx=idx, count=one)
+    keys = [torch.empty(1, 8, 132, dtype=torch.uint8, **meta)]
+    with pytest.raises(ValueError, match="32 bits"):
+        fm.fm_index_append(q, keys, one, one, N=5 - (1 << 32))
