@@ -641,7 +641,8 @@ fm_status fm_add_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residu
 /* Synchronises `stream` and returns FM_ERR_DEVICE if a kernel launched on this
  * context recorded an error since the last call (the record is cleared), or
  * if one of the context-free kernels of the current device did (decode
- * attention, compaction, gather: a bounded wait that ran out), FM_ERR_CUDA
+ * attention, compaction, gather, the attention over the 4-bit cache: a bounded
+ * wait that ran out), FM_ERR_CUDA
  * if the stream reports a CUDA error, FM_OK otherwise. */
 fm_status fm_sync_status(fm_ctx* ctx, cudaStream_t stream);
 
