@@ -561,7 +561,8 @@ fm_status fm_kv4_append(const fm_kv4_cache* cache, const fm_kv4_append_desc* d, 
  *
  * Scores, and the factor of a score (scale * 2^e for queries of size 2^e, over a
  * cap, times a key's scale), count as infinite and as the largest float past
- * fp32's range.  A cap is within 2^-22 of itself in 16-bit calls up to a cap of
+ * fp32's range; a query with a NaN or (without a cap) an infinity gives NaN, and
+ * one whose scores are all minus infinity 0.  A cap is within 2^-22 of itself in 16-bit calls up to a cap of
  * 64, and within two units of tanh beyond and in fp32. */
 typedef struct fm_kv4_attn_desc {
   int dtype;                  /* FM_F32, FM_BF16, FM_F16: of q and out */

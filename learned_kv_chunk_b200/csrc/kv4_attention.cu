@@ -616,12 +616,15 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
       }
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      for (int i = 0; i < 32; ++i) m = fmax_nan(m, fabsf(v[i]));
+      m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmax_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int e = max(-110, min(120, (int)(__float_as_uint(m) >> 23) - 127 - 7));  // m * 2^-e in [2^7, 2^8)
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      const float c = bounded(a.coef * __uint_as_float((uint32_t)(127 + e) << 23));
+      // (one that is not finite makes its scores NaN, as scores of minus infinity alone would pass for masked ones;
+      // a cap turns infinite scores into finite ones)
+      const bool finite = m < INFINITY;
+      const float c = finite || a.softcap > 0.f ? bounded(a.coef * __uint_as_float((uint32_t)(127 + e) << 23)) : nan_f32();
       if constexpr (kQReg) {
         coef[0][0] = __shfl_sync(0xffffffffu, c, 8 * t);
         coef[0][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(Shape<NT, P>::kThreads, kCtas) kv4_attn_kernel
           const float x = v[4 * j + 2 * i] * down, y = v[4 * j + 2 * i + 1] * down;
           hi[i] = pack_f16(x, y);
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-          lo[i] = pack_f16(x - f.x, y - f.y);
+          lo[i] = finite ? pack_f16(x - f.x, y - f.y) : 0u;
         }
         if constexpr (kQReg) {
           qf[0][j][0] = hi[0];

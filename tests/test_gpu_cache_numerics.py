@@ -278,3 +278,31 @@ def test_groups_far_below_their_record(dtype, below):
     half = torch.finfo(TYPES[dtype]).eps / 2
     tol = (2 * dx + w) * abs_v + lost * np.abs(v).max() + top_v + half * np.abs(ref)
     assert (np.abs(o.double().cpu().numpy() - ref) <= tol).all()
+
+
+# ------------------------------------------------------ queries not finite
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("tokens,Hq", [(30, 4), (30, 12), (3000, 4), (3000, 12)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_a_query_that_is_not_finite_gives_nan_and_the_others_do_not(dtype, tokens, Hq, bad):
+    """Its scores are infinite or NaN, whichever sign the keys give them; one that sees nothing gives 0 all the same."""
+    rng = np.random.default_rng(10)
+    kp, vp, table = make_cache(rng, [tokens, 1], 1, PAGE)
+    kp[:, :, :PAGE * 64:64] = (kp[:, :, :PAGE * 64:64] & 0xf0) | 3  # dim 0 of every key: 1.5 of its scale
+    q = torch.from_numpy(rng.standard_normal((2, 2, Hq, 128))).to(TYPES[dtype])
+    good = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.array([tokens, 1], np.int32)))
+    q[:, :, 1, 0] = bad
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.array([tokens, 1], np.int32)))
+    assert bool(torch.isnan(o[0, :, 1]).all()) and bool(torch.isnan(o[1, 1, 1]).all())
+    assert not o[1, 0].any()  # before the row's start
+    rest = [h for h in range(Hq) if h != 1]
+    assert torch.equal(o[:, :, rest], good[:, :, rest])
+    if bad == bad:  # a cap makes the scores cap or -cap: all the same here, and the output the mean
+        o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), dev(np.array([tokens, 1], np.int32)), softcap=30.0)
+        v, _ = OC.read_cache(vp, table, PAGE)
+        for t in range(2):
+            seen = v[0, 0, :tokens - 1 + t]
+            tol = (2.0 ** -18 if dtype == "fp32" else 2.0 ** -11 + 2.0 ** -8) * np.abs(seen).mean(0) + 2.0 ** -23 * tokens / 16
+            assert (np.abs(o[0, t, 1].double().cpu().numpy() - seen.mean(0)) <= tol).all()
