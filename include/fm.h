@@ -461,9 +461,10 @@ fm_status fm_toy_decoder_update(const float* hidden, const float* attn_out, int 
  *            half) and four e8m0 scales, one for each 32 dimensions:
  *            value = e2m1(code) * 2^(scale - 127).  The stored scale byte is
  *            the least that keeps the group's largest magnitude within 6
- *            times the scale, at least 1 and at most 252; a group of zeros
- *            has 0, a group with a NaN or an infinity has 255 and reads as
- *            NaN.  Codes are the nearest values, ties to the even code; a
+ *            times the scale, at least 1 and at most 252 (magnitudes past 6 *
+ *            2^125 are held to it); a group of zeros has 0, a group with a NaN
+ *            or an infinity, or a rotated key past fp32's range, has 255 and
+ *            reads as NaN.  Codes are the nearest values, ties to the even code; a
  *            zero has no sign.
  *   block    the records of page_size tokens of one kv head: page_size * 64
  *            code bytes (token after token), then page_size * 4 scale bytes.
@@ -603,7 +604,8 @@ fm_status fm_kv4_attention(const fm_kv4_cache* cache, const fm_kv4_attn_desc* d,
  *   scale = max|x| / 448 in fp32, codes = e4m3(x / scale), nearest even (formed
  *   as x * (448 / max|x|))
  * into record chunk[t] of row row[t] of comp_k[l].  A key whose scale would be
- * below 2^-126 is stored as zeros with scale 0; one with a NaN or an infinity
+ * below 2^-126 is stored as zeros with scale 0; one with a NaN or an infinity,
+ * or whose sums pass fp32's range before the 128^-1/2 (elements past 2^120),
  * gets a NaN scale.  A token with row[t] outside [0, B) or chunk[t] outside
  * [0, N) is padding: nothing is written.  Two tokens of one call must not
  * name the same record, and the layers' tensors must not overlap (the same

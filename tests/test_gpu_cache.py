@@ -834,3 +834,39 @@ def test_attention_into_its_queries_is_the_attention(dtype, lens, Hq, Hkv, Tq):
     got = q.clone()
     fm.fm_kv4_attention(got, kp, vp, table, n, out=got)
     assert torch.equal(want, got)
+
+
+# ------------------------------------------------ where fp32's range ends
+
+
+def test_keys_at_the_end_of_fp32():
+    """Indexer keys up to 2^120 have their records, whatever the transform adds up; a transform past fp32's range
+    gives a NaN scale.  A rotated key past it makes its group NaN, an unrotated one is held to 6 * 2^125."""
+    k = torch.zeros(3, 1, 128)
+    k[0] = 2.0 ** 120
+    k[1] = 2.0 ** 120 * torch.from_numpy(np.random.default_rng(61).choice([-1.0, 1.0], 128)).float()
+    k[2] = 2.0 ** 122
+    comp_k = [torch.zeros(1, 8, 132, device=DEV, dtype=torch.uint8)]
+    fm.fm_index_append(k.to(DEV), comp_k, dev(np.zeros(3, np.int32)), dev(np.arange(3, dtype=np.int32)))
+    codes, scale = records(comp_k[0])
+    for t in range(2):
+        x = OC.index_vector(k[t:t + 1].double().numpy())[0, 0]
+        want = np.abs(x).max() / 448
+        assert abs(scale[0, t] - want) <= 2.0 ** -20 * want
+        tol = np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * want) + 2.0 ** -20 * 448 * want
+        assert (np.abs(codes[0, t] * scale[0, t] - x) <= tol).all()
+    assert np.isnan(scale[0, 2])
+    x = torch.zeros(2, 2, 128)
+    x[:, :, 64:] = 3e38
+    x[:, :, 96:] *= -1
+    x[1] *= 2.0 ** -1
+    kp, vp = (torch.zeros(1, 1, 16 * 68, device=DEV, dtype=torch.uint8) for _ in range(2))
+    g = x.to(DEV)
+    # every pair turned by an eighth: a c - b s = 3e38 * 2^(1/2), b c + a s = 0
+    _, kh, vh = fm.fm_kv4_append(g[:, :1], g[:, 1:], kp, vp, dev(np.zeros((1, 1), np.int32)), dev(np.zeros(2, np.int32)),
+                                 dev(np.arange(2)), inv_freq=dev(np.full(32, math.pi / 4)), positions=dev(np.ones(2, np.int64)),
+                                 values=True)
+    kh, vh = kh.double().cpu().numpy(), vh.double().cpu().numpy()
+    assert np.isnan(kh[0, 0, 64:96]).all() and (np.abs(kh[0, 0, :64]) == 0).all()
+    assert (kh[1, 0, 64:96] == 4 * 2.0 ** 125).all()  # 2.1e38 = 4.99 * 2^125
+    assert (vh[0, 0, 64:96] == 6 * 2.0 ** 125).all() and (vh[0, 0, 96:] == -6 * 2.0 ** 125).all()
