@@ -576,8 +576,10 @@ typedef struct fm_kv4_attn_desc {
   const int32_t* kv_len;      /* [B] device: cached tokens of a row, clamped to [0, max_len] */
   const int32_t* kv_start;    /* [B] device or NULL: the first visible position (a document's start, left padding) */
   int max_len;                /* a bound of kv_len, 1..max_pages * page_size: sizes the launch */
-  const int32_t* idx;         /* [B, max_sel] device or NULL: visible positions (fm_compact_mask's list); one that is
-                                 listed twice counts twice, one outside [0, kv_len) not at all */
+  const int32_t* idx;         /* [B, max_sel] device or NULL: visible cache positions; one that is listed twice
+                                 counts twice, one outside [0, kv_len) not at all.  (fm_compact_mask lists
+                                 chunks: its list as it is where each token is a chunk, otherwise the
+                                 positions that they cover) */
   const int32_t* count;       /* [B] device, with idx: entries of a row, clamped to [0, max_sel] */
   int max_sel;
   float scale;                /* -2^32..2^32 */

@@ -760,8 +760,8 @@ def fm_kv4_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     bf16 or fp16.  scale (128^-1/2), softcap (scores capped by a tanh), slopes
     [n_q_heads] fp32 (a bias slope * (key position - query position)), window
     (positions a query sees back, itself included), kv_start [B] int32 (first
-    visible position), idx / count (fm_compact_mask's list: only the kept
-    positions are read).  max_len bounds kv_len where the caller knows it.
+    visible position), idx / count (a list of cache positions: only those are
+    read; fm_compact_mask's list of kept chunks where each token is a chunk).  max_len bounds kv_len where the caller knows it.
     Returns the output in q's type and shape; 0 for a query that sees nothing."""
     window, max_len = _i32(window, "window"), None if max_len is None else _i32(max_len, "max_len")
     shape, st = q.shape, q.stride()

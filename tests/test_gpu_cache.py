@@ -870,3 +870,33 @@ def test_keys_at_the_end_of_fp32():
     assert np.isnan(kh[0, 0, 64:96]).all() and (np.abs(kh[0, 0, :64]) == 0).all()
     assert (kh[1, 0, 64:96] == 4 * 2.0 ** 125).all()  # 2.1e38 = 4.99 * 2^125
     assert (vh[0, 0, 64:96] == 6 * 2.0 ** 125).all() and (vh[0, 0, 96:] == -6 * 2.0 ** 125).all()
+
+
+# ------------------------------------------------------- chunks of tokens
+
+
+@pytest.mark.parametrize("s", [1, 4])
+def test_kept_chunks_as_the_positions_that_they_cover(s):
+    """A mask over chunks of s tokens, compacted, spread to cache positions and attended to; the last chunk is cut by
+    the row's length, and the newest token, in no chunk yet, is listed by the caller."""
+    rng = np.random.default_rng(71)
+    N, keep_n = 60, 24
+    n_chunks = np.array([50, 13, 0])
+    lens = [50 * s + 1, 13 * s - s // 2, 1]
+    kp, vp, table = make_cache(rng, lens, 2, 16, cap=N * s + 1)
+    keep = np.zeros((3, N), np.uint8)
+    for b, n in enumerate(n_chunks):
+        keep[b, rng.permutation(n)[:min(keep_n, n)]] = 1
+    idx, count = fm.fm_compact_mask(dev(keep), keep_n)
+    at = (idx[:, :, None] * s + torch.arange(s, device=DEV, dtype=torch.int32)).flatten(1)
+    n = dev(np.asarray(lens, np.int32))
+    new = torch.where(torch.tensor([True, False, True], device=DEV), n - 1, -1)
+    at = torch.cat([new.view(3, 1), at], dim=1).contiguous()
+    q = torch.from_numpy(rng.standard_normal((3, 1, 8, 128))).bfloat16()
+    o = fm.fm_kv4_attention(q.to(DEV), dev(kp), dev(vp), dev(table), n, idx=at, count=count * s + 1)
+    want = np.full((3, N * s + 1), -1)
+    total = np.zeros(3, int)
+    for b in range(3):
+        seen = [c * s + i for c in np.flatnonzero(keep[b]) for i in range(s)] + ([lens[b] - 1] if b != 1 else [])
+        want[b, :len(seen)], total[b] = seen, len(seen)
+    check_attention(o, q, kp, vp, table, lens, 16, idx=want, count=total)
