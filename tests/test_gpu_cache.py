@@ -900,3 +900,62 @@ def test_kept_chunks_as_the_positions_that_they_cover(s):
         seen = [c * s + i for c in np.flatnonzero(keep[b]) for i in range(s)] + ([lens[b] - 1] if b != 1 else [])
         want[b, :len(seen)], total[b] = seen, len(seen)
     check_attention(o, q, kp, vp, table, lens, 16, idx=want, count=total)
+
+
+# ------------------------------------------------ captured, and on another stream
+
+
+def test_a_whole_step_captured_and_on_another_stream():
+    """Norm, appends and attention as one graph, replayed with new inputs and positions, and the same calls on a
+    stream of the caller's: all give the bits of the eager step."""
+    rng = np.random.default_rng(81)
+    B, N, Hq, Hkv, page = 3, 64, 16, 2, 16
+    freq = fm.fm_rope_frequencies(DEV)
+    table = torch.from_numpy(rng.permutation(B * N // page).reshape(B, -1).astype(np.int32)).to(DEV)
+    seq = torch.arange(B, device=DEV, dtype=torch.int32)
+
+    def fresh():
+        return [torch.zeros(B * N // page, Hkv, page * 68, device=DEV, dtype=torch.uint8) for _ in range(2)] + [
+            torch.zeros(B, N, 132, device=DEV, dtype=torch.uint8) for _ in range(3)]
+
+    x, r = torch.zeros(B, 1024, device=DEV), torch.zeros(B, 1024, device=DEV)
+    qkv = torch.zeros(B, Hq + 2 * Hkv, 128, device=DEV, dtype=torch.bfloat16)
+    ik = torch.zeros(B, 3, 128, device=DEV, dtype=torch.bfloat16)
+    pos = torch.zeros(B, device=DEV, dtype=torch.int64)
+
+    def step(state, stream=None):
+        kp, vp, *comp = state
+        z, codes, scales = fm.fm_add_rmsnorm_fp8(x, r, stream=stream)
+        q, kh, vh = fm.fm_kv4_append(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], kp, vp, table, seq, pos, inv_freq=freq,
+                                     q=qkv[:, :Hq], values=True, stream=stream)
+        if stream is None:
+            chunk, n = pos.int(), (pos + 1).int()
+        else:
+            with torch.cuda.stream(stream):
+                chunk, n = pos.int(), (pos + 1).int()
+        fm.fm_index_append(ik, comp, seq, chunk, inv_freq=freq, positions=pos, stream=stream)
+        return z, codes, scales, q, kh, vh, fm.fm_kv4_attention(q, kp, vp, table, n, stream=stream)
+
+    eager, graphed, aside = fresh(), fresh(), fresh()
+    step(fresh())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(graphed)
+    for t in graphed:
+        t.zero_()
+    side = torch.cuda.Stream()
+    for i in range(6):
+        for t, shape in ((x, x.shape), (r, r.shape), (qkv, qkv.shape), (ik, ik.shape)):
+            t.copy_(torch.from_numpy(rng.standard_normal(shape)))
+        pos.fill_(5 * i)
+        want = step(eager)
+        g.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(aside, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b, c in zip(want, out, got):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+            assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+        for a, b, c in zip(eager, graphed, aside):
+            assert torch.equal(a, b) and torch.equal(a, c)

@@ -166,3 +166,20 @@ def test_a_window_over_long_rows_and_pages_missing_in_it():
         table[:, -100:-40] = -1
     check(6, [40000] * 8, 64, 8, "bf16", window=20000, table_edit=edit)
     check(6, [40000] * 8, 96, 8, "bf16", window=20000, table_edit=edit)
+
+
+@pytest.mark.parametrize("B,n,G,dtype", [(40, 900, 8, "bf16"), (300, 700, 12, "fp32"), (3000, 60, 2, "bf16"),
+                                         (3000, 60, 24, "fp16")])
+@pytest.mark.parametrize("listed", [False, True])
+def test_more_rows_than_lanes(B, n, G, dtype, listed):
+    """Their places among the CTAs come from the block's scan: rows of every length, with lists and without."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, n + 1, B)]
+    lens[0] = n
+    check(7, lens, G, 1, dtype, page=16, listed=listed)
+
+
+@pytest.mark.parametrize("Tq", [1, 5])
+def test_as_many_heads_as_there_may_be(Tq):
+    check(8, [50, 200], 1024, 1024, "bf16", page=16, Tq=Tq)
+    check(8, [50, 700], 1024, 1, "fp32", page=16, Tq=Tq)
