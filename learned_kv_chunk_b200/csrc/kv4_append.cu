@@ -21,11 +21,11 @@
 //     group's maximum; x * 2^-e is exact.
 //
 // What bounds them.  Small calls: the chain of loads (position, page, record) and
-// the launch, 4.3 us for 64 tokens of 80 heads and for 64 tokens of three indexer
+// the launch, 3.4 us for 64 tokens of 80 heads, 2.8 for 64 tokens of three indexer
 // keys.  Prompts: the instructions of the rotation and the transform, issued in
 // four of five cycles.  8192 tokens of 48 heads (210 MB read and written): 55 us,
 // 3.8 TB/s, where a copy would take 32; 32768 tokens of three indexer keys
-// (39 MB): 21 us, where a copy would take 6.
+// (39 MB): 22 us, where a copy would take 6.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

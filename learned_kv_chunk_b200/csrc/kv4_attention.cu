@@ -23,13 +23,17 @@
 //     while the block before it waits.
 //
 // What bounds it.  The copies alone run at the memory's rate (8 rows of 131072
-// tokens, 8 kv heads: 1.14 GB in 187 us, 6.1 TB/s).  The arithmetic does not hide
-// behind them: 32 tokens of a kv head take 128 conversions, 128 products with the
-// scales, 64 selections and shifts and 32 matrix instructions of a warp, each at
-// two cycles (eight the last), about 590 instructions with the rest, on 14
-// consumer warps an SM: 240 us, 4.75 TB/s.  In short calls the start counts: a
-// warp's first tile takes 9000 to 12000 cycles where later ones take 2000, with
-// its data there or not, and a change of units 8000 (merge, queries).
+// tokens, 8 kv heads: 1.14 GB in 187 us, 6.1 TB/s).  With the arithmetic it is 237
+// us, 4.8 TB/s, and no pipe is full: 58 % of the issue slots, the ALU at 52 %, the
+// tensor pipe at 25 %.  Accumulators and dequantised operands live in the registers
+// of the warps that use them, which leaves 16 warps an SM, and each waits on its
+// own chain: 32 tokens of a kv head are 128 conversions, 128 products with the
+// scales, 64 selections and shifts and 32 matrix instructions, about 590
+// instructions with the rest.  A tile of the general form takes three and
+// a half times as long (4 x 65536 tokens with a group of zeros in every other tile:
+// 160 us, 71 without).  In short calls the start counts: a warp's first tile takes 9000 to
+// 12000 cycles where later ones take 2000, with its data there or not, and a change
+// of units 8000 (merge, queries).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
